@@ -47,6 +47,19 @@ class SgemmCfg(ctypes.Structure):
         return {n: getattr(self, n) for n, _ in self._fields_}
 
 
+# Activations of an epilogue (SGEMM_ACT_* in sgemm_ops.h) by their names here.
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+class SgemmEpilogue(ctypes.Structure):
+    """sgemm_epilogue of sgemm_ops.h; null pointers (None) leave a part out."""
+    _fields_ = [("activation", ctypes.c_int),
+                ("bias", ctypes.c_void_p), ("stride_bias", ctypes.c_longlong)] + [
+        f for name in ("pre", "grad_pre", "residual") for f in (
+            (name, ctypes.c_void_p), (f"ld_{name}", ctypes.c_int),
+            (f"stride_{name}", ctypes.c_longlong))]
+
+
 _libs = {}      # loaded builds by path
 _active = None  # path calls go to while library() is in effect (None: LIB_PATH)
 
@@ -95,6 +108,17 @@ def load(path=None):
         "sgemm_f32_num_variants": [],
         "sgemm_f32_variant": [i, cfgp],
         "sgemm_f32_variant_ops": [i],
+        "sgemm_f32_epilogue": [i, i, i, i, i, f, p, i, ll, p, i, ll, p, i, ll, i,
+                               ctypes.POINTER(SgemmEpilogue), p, sz, p, cfgp],
+        "sgemm_f32_activation_grad": [i, i, i, p, i, p, i, p, i, p, p, sz, p],
+        "sgemm_f32_activation_grad_workspace": [i, i, ctypes.POINTER(sz)],
+        "sgemm_rmsnorm_f32": [i, i, p, i, p, i, p, f, p, i, p, i, p],
+        "sgemm_rmsnorm_e4m3": [i, i, p, i, p, i, p, f, p, i, p, i, p, p],
+        "sgemm_quantize_e4m3": [i, i, p, i, p, i, p, p],
+        "sgemm_rmsnorm_f32_grad": [i, i, p, i, p, i, p, f, p, i, p, i, p, p, sz, p],
+        "sgemm_rmsnorm_f32_grad_workspace": [i, i, ctypes.POINTER(sz)],
+        "sgemm_e4m3": [i, i, i, p, i, p, p, i, p, p, i, ctypes.POINTER(SgemmEpilogue), p, sz, p],
+        "sgemm_e4m3_workspace_size": [i, i, i, ctypes.POINTER(sz)],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -221,6 +245,8 @@ def _row_major_view(t, name):
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if ld < cols:
+        raise ValueError(f"{name}'s rows must not overlap (row stride {ld}, {cols} columns)")
     return rows, cols, max(ld, cols, 1)
 
 

@@ -50,6 +50,7 @@ struct Variant {
                                  // costs (0: one, the fixed cost is paid every round)
     int ld64;                    // addresses its operands in 64 bits throughout: any
                                  // leading dimension (0: the tile limits below apply)
+    const void *fn_epi[4];       // the forms with an epilogue (null: none)
 };
 
 // One call as the planner sees it.
@@ -477,8 +478,10 @@ inline bool can_split(const Problem &q, long long workspace_bytes)
 // on how many compute units stream at once (which the model does not
 // capture), and with a workspace a split over larger tiles reaches the same
 // parallelism with fewer bytes.
+// epilogue: only variants with a form that applies one.  Its cost is left
+// out: it is the same few passes over C whichever plan runs.
 inline Choice select_plan(const Variant *vs, int n, const Problem &p, int cus, bool aligned16,
-                          bool lds_ok, long long workspace_bytes)
+                          bool lds_ok, long long workspace_bytes, bool epilogue = false)
 {
     const int op = op_index(p);
     Choice best = {-1, 1, 0, 0};
@@ -487,7 +490,8 @@ inline Choice select_plan(const Variant *vs, int n, const Problem &p, int cus, b
         for (int i = 0; i < n; ++i) {
             const Variant &v = vs[i];
             if (v.eff_permille <= 0 || v.eff_one_permille <= 0 ||
-                v.eff_unaligned_permille <= 0 || !v.fn[op] || !variant_fits(v, p))
+                v.eff_unaligned_permille <= 0 || !v.fn[op] || !variant_fits(v, p) ||
+                (epilogue && !v.fn_epi[op]))
                 continue;
             const int eff = variant_eff(v, aligned16, lds_ok, pass == 0);
             if (eff <= 0) continue;

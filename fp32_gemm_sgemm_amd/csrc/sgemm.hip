@@ -14,6 +14,10 @@
 #include <mutex>
 
 #include "sgemm.h"
+#include "sgemm_ops.h"
+#include "epilogue.hpp"
+#include "rowops.hpp"
+#include "gemm_e4m3.hpp"
 #include "sgemm_mfma.hpp"
 #include "sgemm_mfma_dl.hpp"
 #include "sgemm_mfma_sk.hpp"
@@ -66,6 +70,18 @@ Variant dl_variant(int eff_permille, int eff_one_permille, int eff_unaligned_per
     if constexpr ((OPS & 8) != 0)
         v.fn[3] = reinterpret_cast<const void *>(
             &sgemm::sgemm_mfma_dl_kernel<BM, BN, BK, WM, WN, STAGES, true, true, DW, PIPE, MB>);
+    // every layout compiled above has its form with an epilogue
+    v.fn_epi[0] = reinterpret_cast<const void *>(
+        &sgemm::sgemm_mfma_dl_kernel<BM, BN, BK, WM, WN, STAGES, false, false, DW, PIPE, MB, true>);
+    if constexpr ((OPS & 2) != 0)
+        v.fn_epi[1] = reinterpret_cast<const void *>(
+            &sgemm::sgemm_mfma_dl_kernel<BM, BN, BK, WM, WN, STAGES, true, false, DW, PIPE, MB, true>);
+    if constexpr ((OPS & 4) != 0)
+        v.fn_epi[2] = reinterpret_cast<const void *>(
+            &sgemm::sgemm_mfma_dl_kernel<BM, BN, BK, WM, WN, STAGES, false, true, DW, PIPE, MB, true>);
+    if constexpr ((OPS & 8) != 0)
+        v.fn_epi[3] = reinterpret_cast<const void *>(
+            &sgemm::sgemm_mfma_dl_kernel<BM, BN, BK, WM, WN, STAGES, true, true, DW, PIPE, MB, true>);
     return v;
 }
 
@@ -84,7 +100,11 @@ Variant sk_variant(int eff_permille, int eff_one_permille, int eff_unaligned_per
                     reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, false, true, MB>),
                     reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, true, true, MB>)},
                    eff_permille, eff_one_permille, eff_unaligned_permille, fixed_ns,
-                   spill_permille, spill_full_permille, coresident, 1};
+                   spill_permille, spill_full_permille, coresident, 1,
+                   {reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, false, false, MB, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, true, false, MB, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, false, true, MB, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_mfma_sk_kernel<W, true, true, MB, true>)}};
 }
 
 // 8x8 tiles with K split over the lane pairs and W waves of the workgroup,
@@ -101,7 +121,11 @@ Variant vsk_variant(int eff_permille, int eff_one_permille, int eff_unaligned_pe
                     reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, false, true>),
                     reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, true, true>)},
                    eff_permille, eff_one_permille, eff_unaligned_permille, fixed_ns,
-                   spill_permille, spill_full_permille, coresident, 1};
+                   spill_permille, spill_full_permille, coresident, 1,
+                   {reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, false, false, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, true, false, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, false, true, true>),
+                    reinterpret_cast<const void *>(&sgemm::sgemm_valu_sk_kernel<W, true, true, true>)}};
 }
 
 Variant valu_variant()
@@ -266,10 +290,23 @@ struct Call {
     long long sa, sb, sc;
     void *ws;
     size_t ws_bytes;
+    const sgemm::Epi *epi = nullptr;  // the epilogue (null: none; beta is then 0)
 };
 
 // Whether A and B are read at all.
 bool reads_operands(const Call &c) { return c.p.K > 0 && c.alpha != 0.0f; }
+
+// The memory operands A and B span.
+Span operand_a(const Call &c)
+{
+    const Problem &p = c.p;
+    return p.transa ? span(c.A, p.K, p.M, p.lda, c.sa, p.batch) : span(c.A, p.M, p.K, p.lda, c.sa, p.batch);
+}
+Span operand_b(const Call &c)
+{
+    const Problem &p = c.p;
+    return p.transb ? span(c.B, p.N, p.K, p.ldb, c.sb, p.batch) : span(c.B, p.K, p.N, p.ldb, c.sb, p.batch);
+}
 
 hipError_t validate(const Call &c)
 {
@@ -287,16 +324,91 @@ hipError_t validate(const Call &c)
     }
     if (p.K == 0) return hipSuccess;
     if (!c.A || !c.B || misaligned(c.A, 4) || misaligned(c.B, 4)) return hipErrorInvalidValue;
-    const Span as = p.transa ? span(c.A, p.K, p.M, p.lda, c.sa, p.batch)
-                             : span(c.A, p.M, p.K, p.lda, c.sa, p.batch);
-    const Span bs = p.transb ? span(c.B, p.N, p.K, p.ldb, c.sb, p.batch)
-                             : span(c.B, p.K, p.N, p.ldb, c.sb, p.batch);
+    const Span as = operand_a(c), bs = operand_b(c);
     if (overlap(as, cs) || overlap(bs, cs)) return hipErrorInvalidValue;
     if (c.ws_bytes > 0) {
         const Span w{(uintptr_t)c.ws, (uintptr_t)c.ws + c.ws_bytes};
         if (overlap(w, as) || overlap(w, bs)) return hipErrorInvalidValue;
     }
     return hipSuccess;
+}
+
+// One M x N tensor of an epilogue: its row stride, batch stride and alignment.
+bool epi_tensor_ok(const void *ptr, int ld, long long stride, const Problem &p)
+{
+    return ptr && !misaligned(ptr, 4) && ld >= (p.N > 1 ? p.N : 1) && ld <= sgemm::kMaxDim && stride >= 0;
+}
+
+bool overlaps_any(const Span &s, const Span *others, int n)
+{
+    for (int i = 0; i < n; ++i)
+        if (overlap(s, others[i])) return true;
+    return false;
+}
+
+// Checks an epilogue against the M x N output (ldc, stride_c) it belongs to
+// and the `n` spans of memory the call reads or uses as scratch (operands,
+// scales, workspace), and converts it for the kernels.
+hipError_t make_epi(const sgemm_epilogue &s, const Problem &p, const float *C, long long sc,
+                    const Span *used, int n, sgemm::Epi *out)
+{
+    if (s.activation < SGEMM_ACT_NONE || s.activation > SGEMM_ACT_SILU) return hipErrorInvalidValue;
+    if (s.pre && s.grad_pre) return hipErrorInvalidValue;
+    sgemm::Epi e = {};
+    e.act = s.activation;
+    *out = e;
+    if (p.M == 0 || p.N == 0 || p.batch == 0) return hipSuccess;
+    const Span cs = span(C, p.M, p.N, p.ldc, sc, p.batch);
+    constexpr int kMost = 12;
+    Span in[kMost];  // everything the outputs must keep clear of
+    int m = 0;
+    for (int i = 0; i < n; ++i) in[m++] = used[i];
+    if (s.bias) {
+        if (misaligned(s.bias, 4) || s.stride_bias < 0) return hipErrorInvalidValue;
+        in[m++] = span(s.bias, 1, p.N, p.N, s.stride_bias, p.batch);
+        e.bias = s.bias;
+        e.batch_bias = s.stride_bias;
+    }
+    if (s.grad_pre) {
+        if (!epi_tensor_ok(s.grad_pre, s.ld_grad_pre, s.stride_grad_pre, p)) return hipErrorInvalidValue;
+        in[m++] = span(s.grad_pre, p.M, p.N, s.ld_grad_pre, s.stride_grad_pre, p.batch);
+        e.grad_pre = s.grad_pre;
+        e.ld_grad_pre = s.ld_grad_pre;
+        e.batch_grad_pre = s.stride_grad_pre;
+    }
+    if (overlaps_any(cs, in, m)) return hipErrorInvalidValue;
+    if (s.residual) {
+        if (!epi_tensor_ok(s.residual, s.ld_residual, s.stride_residual, p)) return hipErrorInvalidValue;
+        const Span rs = span(s.residual, p.M, p.N, s.ld_residual, s.stride_residual, p.batch);
+        const bool same = s.residual == C && s.ld_residual == p.ldc && (p.batch <= 1 || s.stride_residual == sc);
+        if (overlap(cs, rs) && !same) return hipErrorInvalidValue;
+        // (a workspace is written too)
+        in[m++] = rs;
+        e.residual = s.residual;
+        e.ld_residual = s.ld_residual;
+        e.batch_residual = s.stride_residual;
+    }
+    if (s.pre) {
+        if (!epi_tensor_ok(s.pre, s.ld_pre, s.stride_pre, p)) return hipErrorInvalidValue;
+        if (p.batch > 1 && s.stride_pre < (long long)(p.M - 1) * s.ld_pre + p.N) return hipErrorInvalidValue;
+        const Span ps = span(s.pre, p.M, p.N, s.ld_pre, s.stride_pre, p.batch);
+        if (overlap(ps, cs) || overlaps_any(ps, in, m)) return hipErrorInvalidValue;
+        e.pre = s.pre;
+        e.ld_pre = s.ld_pre;
+        e.batch_pre = s.stride_pre;
+    }
+    *out = e;
+    return hipSuccess;
+}
+
+// Whether a workspace keeps clear of what an epilogue reads (its outputs are
+// checked against it by make_epi).
+bool workspace_clear(const Span &w, const sgemm::Epi &e, const Problem &p)
+{
+    if (e.bias && overlap(w, span(e.bias, 1, p.N, p.N, e.batch_bias, p.batch))) return false;
+    if (e.grad_pre && overlap(w, span(e.grad_pre, p.M, p.N, e.ld_grad_pre, e.batch_grad_pre, p.batch)))
+        return false;
+    return !(e.residual && overlap(w, span(e.residual, p.M, p.N, e.ld_residual, e.batch_residual, p.batch)));
 }
 
 // Rows start 16-byte aligned in every batch entry (a null pointer stands for
@@ -321,8 +433,11 @@ long long max_wgs_per_launch(int threads) { return (long long)(UINT32_MAX / (uin
 hipError_t launch_gemm(const Variant &v, const sgemm_cfg &cfg, const Call &c, hipStream_t stream)
 {
     const Problem &p = c.p;
-    const void *fn = v.fn[sgemm::op_index(p)];
-    GemmArgs g;
+    // a K split's partials are plain products: the reduction applies the epilogue
+    const bool epi = c.epi && cfg.splits <= 1;
+    const void *fn = epi ? v.fn_epi[sgemm::op_index(p)] : v.fn[sgemm::op_index(p)];
+    sgemm::EpiGemmArgs g;
+    if (epi) g.e = *c.epi;
     g.A = c.A;
     g.B = c.B;
     g.batch_a = c.sa;
@@ -360,7 +475,9 @@ hipError_t launch_gemm(const Variant &v, const sgemm_cfg &cfg, const Call &c, hi
     for (long long base = 0; base < cfg.grid; base += per) {
         const long long n = cfg.grid - base < per ? cfg.grid - base : per;
         g.wg_base = (int)base;
-        void *args[] = {&g};
+        // (the plain forms take the GemmArgs that g begins with)
+        GemmArgs &plain = g;
+        void *args[] = {epi ? static_cast<void *>(&g) : static_cast<void *>(&plain)};
         hipError_t e = hipLaunchKernel(fn, dim3((unsigned)n), dim3((unsigned)v.threads), args, 0, stream);
         if (e != hipSuccess) return e;
     }
@@ -388,13 +505,19 @@ hipError_t launch_reduce(const Call &c, int splits, float alpha, hipStream_t str
     constexpr int kMaxY = 65535;
     for (int z0 = 0; z0 < p.batch; z0 += kMaxY) {
         const int nz = p.batch - z0 < kMaxY ? p.batch - z0 : kMaxY;
-        sgemm::ReduceArgs rz = r;
+        sgemm::EpiReduceArgs rz;
+        static_cast<sgemm::ReduceArgs &>(rz) = r;
+        rz.z0 = z0;
+        if (c.epi) rz.e = *c.epi;
         rz.P = r.P ? r.P + (long long)z0 * r.batch_p : nullptr;
         rz.C = c.C + (long long)z0 * c.sc;
         rz.batch_c = c.sc;
-        void *args[] = {&rz};
-        hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(&sgemm::splitk_reduce_kernel),
-                                       dim3((unsigned)blocks, (unsigned)nz), dim3(256), args, 0, stream);
+        sgemm::ReduceArgs &plain = rz;
+        void *args[] = {c.epi ? static_cast<void *>(&rz) : static_cast<void *>(&plain)};
+        const void *fn = c.epi ? reinterpret_cast<const void *>(&sgemm::splitk_reduce_kernel<true>)
+                               : reinterpret_cast<const void *>(&sgemm::splitk_reduce_kernel<false>);
+        hipError_t e = hipLaunchKernel(fn, dim3((unsigned)blocks, (unsigned)nz), dim3(256), args, 0,
+                                       stream);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -404,13 +527,13 @@ hipError_t launch_reduce(const Call &c, int splits, float alpha, hipStream_t str
 // columns), and the last sn columns of the M - sm rows above them.  The row
 // strip streams op(B), which is k-contiguous when B is transposed; the column
 // strip streams op(A), k-contiguous when A is not.
-const void *strip_kernel(const Problem &p)
+template <bool EPI> const void *strip_kernel(const Problem &p)
 {
     static const void *const fns[4] = {
-        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<false, true>),   // NN
-        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<false, false>),  // TN
-        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<true, true>),    // NT
-        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<true, false>),   // TT
+        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<false, true, EPI>),   // NN
+        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<false, false, EPI>),  // TN
+        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<true, true, EPI>),    // NT
+        reinterpret_cast<const void *>(&sgemm::sgemm_strip_kernel<true, false, EPI>),   // TT
     };
     return fns[sgemm::op_index(p)];
 }
@@ -421,7 +544,11 @@ hipError_t launch_strips(const Call &c, int sm, int sn, int cus, hipStream_t str
     const int m_main = p.M - sm, n_main = p.N - sn;
     // workgroups, order and width of each strip (shared with the cost model)
     const sgemm::StripPlan g = sgemm::strip_plan(p, sm, sn, cus);
-    sgemm::StripArgs a = {};
+    sgemm::EpiStripArgs a = {};
+    if (c.epi) a.e = *c.epi;
+    a.m_main = m_main;
+    a.n_main = n_main;
+    a.N = p.N;
     a.K = p.K;
     a.alpha = c.alpha;
     a.beta = c.beta;
@@ -485,8 +612,10 @@ hipError_t launch_strips(const Call &c, int sm, int sn, int cus, hipStream_t str
     for (int z0 = 0; z0 < p.batch; z0 += kMaxY) {
         const int nz = p.batch - z0 < kMaxY ? p.batch - z0 : kMaxY;
         a.z0 = z0;
-        void *args[] = {&a};
-        hipError_t e = hipLaunchKernel(strip_kernel(p), dim3((unsigned)wgs, (unsigned)nz),
+        sgemm::StripArgs &plain = a;
+        void *args[] = {c.epi ? static_cast<void *>(&a) : static_cast<void *>(&plain)};
+        hipError_t e = hipLaunchKernel(c.epi ? strip_kernel<true>(p) : strip_kernel<false>(p),
+                                       dim3((unsigned)wgs, (unsigned)nz),
                                        dim3(sgemm::kStripThreads), args, 0, stream);
         if (e != hipSuccess) return e;
     }
@@ -507,7 +636,7 @@ Call main_part(const Call &c, int sm, int sn)
 // 2 us of host time, which a stream of small products would pay on every call.
 struct PlanKey {
     Problem p;
-    int cus, aligned16, lds_ok;
+    int cus, aligned16, lds_ok, epilogue;
     long long ws;
 };
 struct PlanEntry {
@@ -519,7 +648,7 @@ constexpr int kPlanCacheEntries = 8;
 thread_local PlanEntry t_plan_cache[kPlanCacheEntries];
 thread_local int t_plan_next;
 
-Choice cached_plan(const Problem &p, int cus, bool aligned16, bool lds_ok, long long ws)
+Choice cached_plan(const Problem &p, int cus, bool aligned16, bool lds_ok, long long ws, bool epilogue)
 {
     PlanKey key;
     memset(&key, 0, sizeof(key));  // padding too: keys compare bytewise
@@ -527,11 +656,13 @@ Choice cached_plan(const Problem &p, int cus, bool aligned16, bool lds_ok, long 
     key.cus = cus;
     key.aligned16 = aligned16 ? 1 : 0;
     key.lds_ok = lds_ok ? 1 : 0;
+    key.epilogue = epilogue ? 1 : 0;
     key.ws = ws;
     for (int i = 0; i < kPlanCacheEntries; ++i)
         if (t_plan_cache[i].valid && memcmp(&t_plan_cache[i].key, &key, sizeof(key)) == 0)
             return t_plan_cache[i].choice;
-    const Choice ch = sgemm::select_plan(kVariants, kNumVariants, p, cus, aligned16, lds_ok, ws);
+    const Choice ch = sgemm::select_plan(kVariants, kNumVariants, p, cus, aligned16, lds_ok, ws,
+                                         epilogue);
     PlanEntry &e = t_plan_cache[t_plan_next];
     t_plan_next = (t_plan_next + 1) % kPlanCacheEntries;
     e.key = key;
@@ -545,7 +676,7 @@ int plan_for(const Call &c, int cus, sgemm_cfg *out)
     if (!out || !sgemm::sizes_ok(c.p)) return hipErrorInvalidValue;
     const long long ws = c.ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)c.ws_bytes;
     const Choice ch = cached_plan(c.p, cus > 0 ? cus : 256, rows_aligned16(c),
-                                  sgemm::direct_lds_ok(c.p), ws);
+                                  sgemm::direct_lds_ok(c.p), ws, c.epi != nullptr);
     if (ch.id < 0) return hipErrorInvalidValue;
     return sgemm::finish_cfg(kVariants[ch.id], ch.id, c.p, ch.splits, ch.strip_m, ch.strip_n, out)
                ? hipSuccess
@@ -577,11 +708,12 @@ int run(const Call &c, hipStream_t stream, const sgemm_cfg *force)
     if (force) {
         const int r = forced_cfg(p, force, &cfg);
         if (r != hipSuccess) return r;
+        if (c.epi && !kVariants[cfg.id].fn_epi[sgemm::op_index(p)]) return hipErrorInvalidValue;
     }
     if (p.M == 0 || p.N == 0 || p.batch == 0) return hipSuccess;
     if (!reads_operands(c)) {
         // alpha * (empty or ignored product) + beta * C
-        if (c.beta == 1.0f) return hipSuccess;
+        if (c.beta == 1.0f && !c.epi) return hipSuccess;
         return launch_reduce(c, 0, 0.0f, stream);
     }
     int id = 0;
@@ -624,6 +756,9 @@ Call make_call(int transa, int transb, int M, int N, int K, float alpha,
     c.ws_bytes = ws ? ws_bytes : 0;
     return c;
 }
+
+#include "rowops_host.hpp"
+#include "gemm_e4m3_host.hpp"
 
 }  // namespace
 
@@ -767,6 +902,103 @@ int sgemm_f32(int M, int N, int K, const float *A, int lda, const float *B, int 
 {
     return sgemm_f32_ex(SGEMM_OP_N, SGEMM_OP_N, M, N, K, 1.0f, A, lda, 0, B, ldb, 0, 0.0f, C, ldc, 0, 1,
                         nullptr, 0, stream, nullptr);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+int sgemm_f32_epilogue(int transa, int transb, int M, int N, int K, float alpha,
+                       const float *A, int lda, long long stride_a,
+                       const float *B, int ldb, long long stride_b,
+                       float *C, int ldc, long long stride_c, int batch, const sgemm_epilogue *epi,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream, const sgemm_cfg *cfg)
+{
+    Call c = make_call(transa, transb, M, N, K, alpha, A, lda, stride_a, B, ldb, stride_b, 0.0f,
+                       C, ldc, stride_c, batch, workspace, workspace_bytes);
+    const hipError_t v = validate(c);
+    if (v != hipSuccess) return v;
+    sgemm::Epi e = {};
+    const sgemm_epilogue none = {};
+    Span used[3];
+    int n = 0;
+    if (M > 0 && N > 0 && batch > 0) {
+        if (K > 0) {
+            used[n++] = operand_a(c);
+            used[n++] = operand_b(c);
+        }
+        if (c.ws_bytes > 0) used[n++] = Span{(uintptr_t)c.ws, (uintptr_t)c.ws + c.ws_bytes};
+    }
+    const hipError_t x = make_epi(epi ? *epi : none, c.p, C, stride_c, used, n, &e);
+    if (x != hipSuccess) return x;
+    if (c.ws_bytes > 0 && n > 0 && !workspace_clear(used[n - 1], e, c.p)) return hipErrorInvalidValue;
+    c.epi = &e;
+    return run(c, stream, cfg);
+}
+
+int sgemm_f32_activation_grad(int M, int N, int activation, const float *dY, int ldy, const float *Z, int ldz,
+                              float *dZ, int lddz, float *dbias, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream)
+{
+    return run_act_grad(M, N, activation, dY, ldy, Z, ldz, dZ, lddz, dbias, workspace, workspace_bytes, stream);
+}
+
+int sgemm_f32_activation_grad_workspace(int M, int N, size_t *bytes)
+{
+    if (!bytes || M < 0 || N < 0 || M > sgemm::kMaxDim || N > sgemm::kMaxDim) return hipErrorInvalidValue;
+    *bytes = M > 0 && N > 0 ? parts_bytes(col_plan(M, N).chunks, N) : 0;
+    return hipSuccess;
+}
+
+int sgemm_rmsnorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr, const float *w, float eps,
+                      float *S, int lds, float *Y, int ldy, hipStream_t stream)
+{
+    return run_row(true, false, rows, D, X, ldx, R, ldr, w, eps, S, lds, Y, ldy, nullptr, 0, nullptr, stream);
+}
+
+int sgemm_rmsnorm_e4m3(int rows, int D, const float *X, int ldx, const float *R, int ldr, const float *w, float eps,
+                       float *S, int lds, void *Q, int ldq, float *scale, hipStream_t stream)
+{
+    return run_row(true, true, rows, D, X, ldx, R, ldr, w, eps, S, lds, nullptr, 0, Q, ldq, scale, stream);
+}
+
+int sgemm_quantize_e4m3(int rows, int D, const float *X, int ldx, void *Q, int ldq, float *scale,
+                        hipStream_t stream)
+{
+    return run_row(false, true, rows, D, X, ldx, nullptr, 0, nullptr, 0.0f, nullptr, 0, nullptr, 0, Q, ldq, scale,
+                   stream);
+}
+
+int sgemm_rmsnorm_f32_grad(int rows, int D, const float *dY, int ldy, const float *S, int lds, const float *w,
+                           float eps, const float *dS, int ldds, float *dX, int lddx, float *dw, void *workspace,
+                           size_t workspace_bytes, hipStream_t stream)
+{
+    return run_row_grad(rows, D, dY, ldy, S, lds, w, eps, dS, ldds, dX, lddx, dw, workspace, workspace_bytes,
+                        stream);
+}
+
+int sgemm_rmsnorm_f32_grad_workspace(int rows, int D, size_t *bytes)
+{
+    if (!bytes || !row_sizes_ok(rows, D, 0.0f)) return hipErrorInvalidValue;
+    *bytes = rows > 0 ? row_grad_bytes(rows, D) : 0;
+    return hipSuccess;
+}
+
+int sgemm_e4m3(int M, int N, int K, const void *A, int lda, const float *scale_a, const void *B, int ldb,
+               const float *scale_b, float *C, int ldc, const sgemm_epilogue *epi, void *workspace,
+               size_t workspace_bytes, hipStream_t stream)
+{
+    return run_e4m3(M, N, K, A, lda, scale_a, B, ldb, scale_b, C, ldc, epi, workspace, workspace_bytes, stream);
+}
+
+int sgemm_e4m3_workspace_size(int M, int N, int K, size_t *bytes)
+{
+    if (!bytes || !e4m3_sizes_ok(M, N, K)) return hipErrorInvalidValue;
+    int cus = 0;
+    const hipError_t e = device_cus(&cus);
+    if (e != hipSuccess) return e;
+    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)e4m3_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
+    return hipSuccess;
 }
 
 }  // extern "C"

@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace sgemm {
 
@@ -175,6 +176,13 @@ struct DlOperand {
         return idx < lim ? 4u * ((uint32_t)r * (uint32_t)ld + (uint32_t)c) : kOobOffset;
     }
 
+    // The row and column (in units of a float) that load j of this lane brings
+    // in, relative to the slice's base.
+    __device__ __forceinline__ static void place(int j, int wave, int lane, int &r, int &c)
+    {
+        source(j, wave, lane, r, c);
+    }
+
   private:
     // The global row r and column c (of the operand as stored, relative to the
     // slice's base) whose EL floats load j of this lane brings in.
@@ -214,10 +222,11 @@ struct DlTraits {
 };
 
 
+// EPI: the form with an epilogue (epilogue.hpp), launched only without a K split.
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int STAGES, bool TA, bool TB, bool DW,
-          int PIPE = 0, int MB = 32>
+          int PIPE = 0, int MB = 32, bool EPI = false>
 __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64)
-sgemm_mfma_dl_kernel(GemmArgs g)
+sgemm_mfma_dl_kernel(typename KernelArgs<EPI>::T g)
 {
     typedef DlTraits<BM, BN, BK, WAVES_M, WAVES_N, STAGES, TA, TB, DW, MB> T;
     typedef typename T::OpA OpA;
@@ -632,20 +641,62 @@ sgemm_mfma_dl_kernel(GemmArgs g)
     // of a 32x32 block, D[4*h + r][l & 15] of a 16x16 one (h as above): C row
     // wave_offset + RM*(that row) + i, column wave_offset + NB*(l mod MB) + j,
     // so a lane holds NB adjacent columns.
-    float *__restrict__ C = g.C;
-    const int ldc = g.ldc;
-    const int col = n0 + wn * WTN + NB * l31;
+    if constexpr (EPI) {
+        // Each wave stages CR accumulators of its blocks at a time (CROWS rows
+        // of WTN results) in its own share of LDS, once every wave has read
+        // the last slice; no other wave touches that share, so the wave's own
+        // LDS order is enough from there on.
+        constexpr int SHARE = T::LDS_FLOATS / NW;
+        constexpr int CR = MB * WTN <= SHARE ? ACC : ACC / 2;
+        constexpr int CROWS = MB / (ACC / CR);
+        static_assert(CROWS * WTN <= SHARE && SHARE % 4 == 0, "a wave's share holds one chunk");
+        static_assert(MB == 32 || CR == ACC, "16x16 blocks are staged whole");
+        typedef float vec_t __attribute__((ext_vector_type(NB)));
+        __syncthreads();
+        float *const mine = smem + wave * SHARE;
+        const StagedEpi<CROWS, WTN, RM, false> epi(g, w.batch, lane, n0 + wn * WTN);
 #pragma unroll
-    for (int i = 0; i < RM; ++i) {
+        for (int i = 0; i < RM; ++i) {
 #pragma unroll
-        for (int r = 0; r < ACC; ++r) {
-            const int row = m0 + wm * WTM +
-                            RM * (MB == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * h + r) + i;
-            if (row >= M) continue;
-            float v[NB];
+            for (int r0 = 0; r0 < ACC; r0 += CR) {
+                if constexpr (kLdsPoison) {
+                    lds_poison(mine + lane * (SHARE / 64), SHARE / 64);
+                    lds_poison_done();
+                }
 #pragma unroll
-            for (int j = 0; j < NB; ++j) v[j] = acc[i][j][r];
-            store_row<NB>(C + (int64_t)row * ldc + col, col, N, v, g.alpha, g.beta);
+                for (int r = r0; r < r0 + CR; ++r) {
+                    const int rr = MB == 32 ? 8 * ((r - r0) >> 2) + 4 * h + (r & 3) : 4 * h + r;
+                    float *p = mine + rr * WTN + NB * l31;
+                    if constexpr (NB == 1) {
+                        *p = acc[i][0][r];
+                    } else {
+                        vec_t v;
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) v[j] = acc[i][j][r];
+                        *reinterpret_cast<vec_t *>(p) = v;
+                    }
+                }
+                asm volatile("" ::: "memory");
+                epi.store(mine, m0 + wm * WTM + RM * (MB / ACC) * r0 + i, 1.0f);
+                asm volatile("" ::: "memory");
+            }
+        }
+    } else {
+        float *__restrict__ C = g.C;
+        const int ldc = g.ldc;
+        const int col = n0 + wn * WTN + NB * l31;
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+#pragma unroll
+            for (int r = 0; r < ACC; ++r) {
+                const int row = m0 + wm * WTM +
+                                RM * (MB == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * h + r) + i;
+                if (row >= M) continue;
+                float v[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) v[j] = acc[i][j][r];
+                store_row<NB>(C + (int64_t)row * ldc + col, col, N, v, g.alpha, g.beta);
+            }
         }
     }
 #if SGEMM_TIMELINE

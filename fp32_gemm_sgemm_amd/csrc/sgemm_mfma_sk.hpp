@@ -35,6 +35,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace sgemm {
 
@@ -48,8 +49,8 @@ template <int W, int MB = 32> struct SkTraits {
     static constexpr int DEPTH = 4;  // k groups in flight per wave
 };
 
-template <int W, bool TA, bool TB, int MB = 32>
-__global__ void __launch_bounds__(W * 64) sgemm_mfma_sk_kernel(GemmArgs g)
+template <int W, bool TA, bool TB, int MB = 32, bool EPI = false>
+__global__ void __launch_bounds__(W * 64) sgemm_mfma_sk_kernel(typename KernelArgs<EPI>::T g)
 {
     typedef SkTraits<W, MB> T;
     constexpr int D = T::DEPTH, REGS = T::REGS, GK = T::GK;
@@ -177,7 +178,13 @@ __global__ void __launch_bounds__(W * 64) sgemm_mfma_sk_kernel(GemmArgs g)
         const int col = n0 + (ln & (MB - 1));
         if (row < M && col < N) {
             float *p = C + (int64_t)row * ldc + col;
-            *p = g.beta != 0.0f ? g.alpha * s + g.beta * *p : g.alpha * s;
+            if constexpr (EPI) {
+                float v[1] = {g.alpha * s};
+                epi_apply<1>(g.e, wk.batch, row, col, N, v);
+                *p = v[0];
+            } else {
+                *p = g.beta != 0.0f ? g.alpha * s + g.beta * *p : g.alpha * s;
+            }
         }
     }
 }

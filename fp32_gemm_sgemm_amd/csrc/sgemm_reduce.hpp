@@ -16,6 +16,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace sgemm {
 
@@ -30,7 +31,17 @@ struct ReduceArgs {
     float alpha, beta;
 };
 
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(ReduceArgs r)
+// With an epilogue: z0 is the batch entry of the launch's first.
+struct EpiReduceArgs : ReduceArgs {
+    Epi e;
+    int z0;
+};
+template <bool EPI> struct ReduceKernelArgs { typedef ReduceArgs T; };
+template <> struct ReduceKernelArgs<true> { typedef EpiReduceArgs T; };
+
+// EPI: C = epilogue(alpha * (the sum)) instead; beta is not used.
+template <bool EPI = false>
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(typename ReduceKernelArgs<EPI>::T r)
 {
     const int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (q >= r.quads) return;
@@ -46,8 +57,16 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(ReduceArgs r)
 #pragma unroll 4
         for (int t = 1; t < r.splits; ++t) s += *reinterpret_cast<const f32x4 *>(p + t * r.split_p);
     }
-    const float v[4] = {s[0], s[1], s[2], s[3]};
-    store_row<4>(r.C + z * r.batch_c + (int64_t)row * r.ldc + col, col, r.N, v, r.alpha, r.beta);
+    if constexpr (EPI) {
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = r.alpha * s[j];
+        epi_apply<4>(r.e, r.z0 + z, row, col, r.N, v);
+        store_row<4>(r.C + z * r.batch_c + (int64_t)row * r.ldc + col, col, r.N, v, 1.0f, 0.0f);
+    } else {
+        const float v[4] = {s[0], s[1], s[2], s[3]};
+        store_row<4>(r.C + z * r.batch_c + (int64_t)row * r.ldc + col, col, r.N, v, r.alpha, r.beta);
+    }
 }
 
 }  // namespace sgemm

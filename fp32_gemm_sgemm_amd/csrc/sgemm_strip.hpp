@@ -47,6 +47,7 @@
 #pragma once
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace sgemm {
 
@@ -84,10 +85,36 @@ struct StripArgs {
     float alpha, beta;
 };
 
-template <bool KC>
-__device__ __forceinline__ void strip_block(const Strip &s, int wg, int K, int z, float alpha,
-                                            float beta, f32x4 *stage)
+// With an epilogue: strip 0 holds rows m_main .. of C, strip 1 columns n_main
+// .. of the rows above (N columns in all).
+struct EpiStripArgs : StripArgs {
+    Epi e;
+    int m_main, n_main, N;
+};
+template <bool EPI> struct StripKernelArgs { typedef StripArgs T; };
+template <> struct StripKernelArgs<true> { typedef EpiStripArgs T; };
+
+// One output: out(x, y) of strip `which` (0 or 1) from its sum over k.
+template <bool EPI>
+__device__ __forceinline__ void strip_store(const typename StripKernelArgs<EPI>::T &a, int which, int z,
+                                            int x, int y, float sum, float *p)
 {
+    if constexpr (EPI) {
+        const int row = which == 0 ? a.m_main + y : x, col = which == 0 ? x : a.n_main + y;
+        float v[1] = {a.alpha * sum};
+        epi_apply<1>(a.e, z, row, col, a.N, v);
+        *p = v[0];
+    } else {
+        *p = a.beta != 0.0f ? a.alpha * sum + a.beta * *p : a.alpha * sum;
+    }
+}
+
+template <bool KC, int WHICH, bool EPI>
+__device__ __forceinline__ void strip_block(const typename StripKernelArgs<EPI>::T &a, int wg, int z,
+                                            f32x4 *stage)
+{
+    const Strip &s = a.s[WHICH];
+    const int K = a.K;
     const float *__restrict__ big = s.big + z * s.batch_big;
     const float *__restrict__ small = s.small + z * s.batch_small;
     const int tid = threadIdx.x, lane = tid & 63;
@@ -250,7 +277,7 @@ __device__ __forceinline__ void strip_block(const Strip &s, int wg, int K, int z
                 if (q < KCP) sum += red[(g + XQ * q) * 16 + i * 4 + y];
             if (x0 + xi < X && y < s.r) {
                 float *p = out + (int64_t)(x0 + xi) * s.o_x + (int64_t)y * s.o_y;
-                *p = beta != 0.0f ? alpha * sum + beta * *p : alpha * sum;
+                strip_store<EPI>(a, WHICH, z, x0 + xi, y, sum, p);
             }
         }
     } else {
@@ -277,21 +304,23 @@ __device__ __forceinline__ void strip_block(const Strip &s, int wg, int K, int z
             for (int w = 1; w < kStripWaves; ++w) sum += red[(w * XQ + q) * 16 + y * 4 + e];
             if (x0 + xi < X && y < s.r) {
                 float *p = out + (int64_t)(x0 + xi) * s.o_x + (int64_t)y * s.o_y;
-                *p = beta != 0.0f ? alpha * sum + beta * *p : alpha * sum;
+                strip_store<EPI>(a, WHICH, z, x0 + xi, y, sum, p);
             }
         }
     }
 }
 
-// KC0, KC1: storage order of strip 0's and strip 1's big operand.
-template <bool KC0, bool KC1>
-__global__ void __launch_bounds__(kStripThreads) sgemm_strip_kernel(StripArgs a)
+// KC0, KC1: storage order of strip 0's and strip 1's big operand.  EPI: with
+// an epilogue (beta is not used).
+template <bool KC0, bool KC1, bool EPI = false>
+__global__ void __launch_bounds__(kStripThreads)
+sgemm_strip_kernel(typename StripKernelArgs<EPI>::T a)
 {
     __shared__ __attribute__((aligned(16))) f32x4 stage[4 * kStripPlane];
     const int z = a.z0 + blockIdx.y;
     const int wg = blockIdx.x;
-    if (wg < a.s[0].wgs) strip_block<KC0>(a.s[0], wg, a.K, z, a.alpha, a.beta, stage);
-    else strip_block<KC1>(a.s[1], wg - a.s[0].wgs, a.K, z, a.alpha, a.beta, stage);
+    if (wg < a.s[0].wgs) strip_block<KC0, 0, EPI>(a, wg, z, stage);
+    else strip_block<KC1, 1, EPI>(a, wg - a.s[0].wgs, z, stage);
 }
 
 }  // namespace sgemm

@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "common.hpp"
+#include "epilogue.hpp"
 
 namespace sgemm {
 
@@ -315,8 +316,8 @@ __device__ __forceinline__ float vsk_kk(const GemmArgs &g, int m0, int n0, int w
     return v[0];
 }
 
-template <int W, bool TA, bool TB>
-__global__ void __launch_bounds__(W * 64) sgemm_valu_sk_kernel(GemmArgs g)
+template <int W, bool TA, bool TB, bool EPI = false>
+__global__ void __launch_bounds__(W * 64) sgemm_valu_sk_kernel(typename KernelArgs<EPI>::T g)
 {
     typedef VskTraits<W> T;
     constexpr bool KK = !TA && TB;  // both operands k-contiguous
@@ -349,7 +350,13 @@ __global__ void __launch_bounds__(W * 64) sgemm_valu_sk_kernel(GemmArgs g)
         const int col = n0 + (KK ? tid & 7 : (tid >> 1) & 7);
         if (row < g.M && col < g.N) {
             float *p = g.C + (int64_t)row * g.ldc + col;
-            *p = g.beta != 0.0f ? g.alpha * s + g.beta * *p : g.alpha * s;
+            if constexpr (EPI) {
+                float v[1] = {g.alpha * s};
+                epi_apply<1>(g.e, wk.batch, row, col, g.N, v);
+                *p = v[0];
+            } else {
+                *p = g.beta != 0.0f ? g.alpha * s + g.beta * *p : g.alpha * s;
+            }
         }
     }
 }
