@@ -429,11 +429,15 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
 // weight rows.  Nothing is shared through LDS but the waves' partial results:
 // every weight is used by one workgroup alone and goes from memory to the
 // registers that feed the MFMA, DEPTH steps ahead; A's few rows are read from
-// L2 by every workgroup.  Rows of A past M and of B past N are read as the last
+// L2 by every workgroup.  One token of an 8192 x 8192 layer takes 13.7 us (4.9
+// TB/s of weights, the launch included), against 12.7 us at the rate of a large
+// copy; 2 steps ahead take 13.8, 4 take 14.5, 4 waves 14.9 and 8 waves 14.4 us,
+// and two column blocks per wave (half of A's reads, half the workgroups) 20.
+// Rows of A past M and of B past N are read as the last
 // one and never stored; codes past K read as zero.
 template <int W, int RM> struct SkinnyTraits {
     static constexpr int NT = W * 64;
-    static constexpr int DEPTH = RM >= 4 ? 2 : 4;
+    static constexpr int DEPTH = 3;
     static constexpr int LDS_FLOATS = W * RM * 256;
 };
 

@@ -29,10 +29,10 @@ template <int BM, int BN, int BKF, int WM, int WN, int MB> const void *e4m3_reg_
 }
 
 const E4m3Variant kE4m3Variants[] = {
-    {256, 256, 512, e4m3_fn<256, 256, 16, 4, 2, 4, 32>(), nullptr, 0.0, 22000.0, 5000.0},
-    {128, 128, 256, e4m3_fn<128, 128, 32, 2, 2, 2, 32>(), e4m3_reg_fn<128, 128, 32, 2, 2, 32>(), 0.0, 5900.0, 3000.0},
-    {64, 128, 256, e4m3_fn<64, 128, 32, 2, 2, 2, 32>(), e4m3_reg_fn<64, 128, 32, 2, 2, 32>(), 600.0, 3400.0, 2000.0},
-    {64, 64, 256, e4m3_fn<64, 64, 32, 2, 2, 2, 16>(), e4m3_reg_fn<64, 64, 32, 2, 2, 16>(), 1500.0, 1900.0, 1700.0},
+    {256, 256, 512, e4m3_fn<256, 256, 16, 4, 2, 4, 32>(), nullptr, 0.0, 22000.0, 5800.0},
+    {128, 128, 256, e4m3_fn<128, 128, 32, 2, 2, 2, 32>(), e4m3_reg_fn<128, 128, 32, 2, 2, 32>(), 0.0, 5900.0, 3800.0},
+    {64, 128, 256, e4m3_fn<64, 128, 32, 2, 2, 2, 32>(), e4m3_reg_fn<64, 128, 32, 2, 2, 32>(), 600.0, 3400.0, 2800.0},
+    {64, 64, 256, e4m3_fn<64, 64, 32, 2, 2, 2, 16>(), e4m3_reg_fn<64, 64, 32, 2, 2, 16>(), 1500.0, 1900.0, 2500.0},
 };
 // Rows that are not 16-byte aligned go through registers: this much slower.
 constexpr double kE4m3RegCost = 1.13;
@@ -42,24 +42,48 @@ constexpr double kE4m3StoreBytesPerNs = 6000.0;
 constexpr double kE4m3ReduceNs = 5000.0;
 constexpr int kE4m3VariantCount = (int)(sizeof(kE4m3Variants) / sizeof(kE4m3Variants[0]));
 
-// Rows of A the streaming kernel serves.
-constexpr int kE4m3SkinnyRows = 64;
-constexpr int kE4m3SkinnyWaves = 8;
+// The streaming kernel for few rows of A, by the rows it holds: its cost is
+// fill_ns plus, per 1024 codes of K, wg_ns + row_ns * M for each workgroup (16
+// columns) of the fullest compute unit, or the weights' time from memory if that is more.
+// Measured (microseconds, launch included) at N x K of 512 x 4096, 1024 x
+// 16384 and 8192 x 8192: 4.9, 11.8 and 13.7 (16 rows: 6.6, 17.1, 17.8) with 2
+// waves; 8.9, 24.7 and 27.2 for 32 rows and 13.2, 39.4 and 43.4 for 64 with 4.
+struct E4m3Skinny {
+    int rows, threads;
+    const void *fn;
+    double wg_ns, row_ns, fill_ns;
+};
+const E4m3Skinny kE4m3Skinny[] = {
+    {16, 128, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<2, 1>), 575.0, 23.0, 100.0},
+    {32, 256, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<4, 2>), 1350.0, 0.0, 1100.0},
+    {64, 256, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<4, 4>), 2200.0, 0.0, 2000.0},
+};
+constexpr int kE4m3SkinnyCount = (int)(sizeof(kE4m3Skinny) / sizeof(kE4m3Skinny[0]));
+constexpr double kE4m3StreamBytesPerNs = 6000.0;
 // Direct loads keep a tile's byte offsets (256 rows and a slice) below 2^31.
 constexpr int kE4m3MaxLdDirect = 1 << 23;
 constexpr int kE4m3SplitAlign = 128;  // codes: whole slices, and 16-byte aligned starts
 
 struct E4m3Plan {
-    int variant;  // -1: the streaming kernel
+    int variant;  // a tile, or the streaming kernel -1 - i
     int splits, k_chunk;
     long long workspace_bytes;
 };
 
 E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws)
 {
-    if (M <= kE4m3SkinnyRows) return {-1, 1, K > 0 ? K : 1, 0};
     E4m3Plan best = {-1, 1, K > 0 ? K : 1, 0};
-    double best_t = 0.0;
+    double best_t = -1.0;
+    for (int i = 0; i < kE4m3SkinnyCount; ++i) {
+        const E4m3Skinny &s = kE4m3Skinny[i];
+        if (M > s.rows) continue;
+        const double per_cu = (double)sgemm::ceil_div_ll(sgemm::ceil_div_ll(N, 16), cus);
+        const double work = (double)K / 1024.0 * per_cu * (s.wg_ns + s.row_ns * M),
+                     stream = (double)N * K / kE4m3StreamBytesPerNs;
+        best = {-1 - i, 1, K > 0 ? K : 1, 0};
+        best_t = s.fill_ns + (work > stream ? work : stream);
+        break;
+    }
     for (int i = 0; i < kE4m3VariantCount; ++i) {
         const E4m3Variant &v = kE4m3Variants[i];
         if (!aligned && !v.reg) continue;
@@ -78,7 +102,7 @@ E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws)
                        4.0 * splits * (double)M * (double)N / kE4m3StoreBytesPerNs;
             if (splits > 1)
                 t += kE4m3ReduceNs + 4.0 * (splits + 1) * (double)M * (double)N / sgemm::kReduceBytesPerNs;
-            if (best.variant < 0 || t < best_t) {
+            if (best_t < 0.0 || t < best_t) {
                 best = {i, splits, splits > 1 ? (int)per : K, bytes};
                 best_t = t;
             }
@@ -163,13 +187,9 @@ hipError_t run_e4m3(int M, int N, int K, const void *A, int lda, const float *sc
     g.alpha = 1.0f;
     g.e = e;
     if (plan.variant < 0) {
-        const void *fn = M <= 16 ? reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<kE4m3SkinnyWaves, 1>)
-                         : M <= 32
-                             ? reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<kE4m3SkinnyWaves, 2>)
-                             : reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<kE4m3SkinnyWaves, 4>);
-        const int threads = 64 * kE4m3SkinnyWaves;
-        const long long wgs = sgemm::ceil_div_ll(N, 16), cap = max_wgs_per_launch(threads);
-        return launch1(fn, dim3((unsigned)(wgs < cap ? wgs : cap)), threads, &g, stream);
+        const E4m3Skinny &s = kE4m3Skinny[-1 - plan.variant];
+        const long long wgs = sgemm::ceil_div_ll(N, 16), cap = max_wgs_per_launch(s.threads);
+        return launch1(s.fn, dim3((unsigned)(wgs < cap ? wgs : cap)), s.threads, &g, stream);
     }
     const E4m3Variant &v = kE4m3Variants[plan.variant];
     g.tiles_m = (int)sgemm::ceil_div_ll(M, v.bm);

@@ -323,8 +323,8 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_grad_kernel(RowGradAr
                     for (int j = 0; j < 4; ++j) g[j] *= u[j];
                 }
             };
-            float g[4], x[4];
             for (int64_t col = 4 * t; col < D; col += 4 * NT) {
+                float g[4], x[4];
                 load((int)col, g, x);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_grad_kernel(RowGradAr
             const float r = 1.0f / sqrtf(sum * inv_d + a.eps);
             const float c = dot * inv_d * r * r * r;
             for (int64_t col = 4 * t; col < D; col += 4 * NT) {
+                float g[4], x[4];
                 load((int)col, g, x);
                 write((int)col, g, x, r, c);
             }
@@ -449,13 +450,17 @@ __global__ void __launch_bounds__(256) col_kernel(ColArgs a)
 }
 
 // out[n] = part[0][n] + part[1][n] + ...: 8 lanes along the columns (32 of
-// them), 32 along the parts, whose sums are added in order.
-__global__ void __launch_bounds__(256) col_sum_kernel(const float *part, int parts, int N, float *out)
+// them) and 128 along the parts, each adding every 128th in order, then their
+// sums in two fixed stages.  The many threads keep the chain of dependent reads
+// short: 1024 parts of 64 columns take 3 us, with 256 threads 8.
+constexpr int kColSumThreads = 1024;
+__global__ void __launch_bounds__(kColSumThreads) col_sum_kernel(const float *part, int parts, int N, float *out)
 {
-    constexpr int TX = 8, TY = 32;
-    __shared__ __attribute__((aligned(16))) float red[TY * TX * 4];
+    constexpr int TX = 8, TY = kColSumThreads / TX, C = 4 * TX, S = 8;  // S sums of TY / S in the first stage
+    __shared__ __attribute__((aligned(16))) float red[TY * C];
+    __shared__ float red2[S * C];
     const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    const int64_t col64 = 4 * ((int64_t)blockIdx.x * TX + tx);
+    const int64_t col64 = (int64_t)C * blockIdx.x + 4 * tx;
     const bool in = col64 < N;
     const int col = in ? (int)col64 : 0;
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -469,19 +474,27 @@ __global__ void __launch_bounds__(256) col_sum_kernel(const float *part, int par
         }
     }
     if constexpr (kLdsPoison) {
-        for (int i = threadIdx.x; i < TY * TX * 4; i += 256) lds_poison(&red[i], 1);
+        for (int i = threadIdx.x; i < TY * C; i += kColSumThreads) lds_poison(&red[i], 1);
+        if (threadIdx.x < S * C) lds_poison(&red2[threadIdx.x], 1);
         lds_poison_done();
         __syncthreads();
     }
-    *reinterpret_cast<f32x4 *>(&red[(ty * TX + tx) * 4]) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+    *reinterpret_cast<f32x4 *>(&red[ty * C + 4 * tx]) = f32x4{sum[0], sum[1], sum[2], sum[3]};
     __syncthreads();
-    if (threadIdx.x >= TX * 4) return;
-    const int64_t c = (int64_t)blockIdx.x * TX * 4 + threadIdx.x;
-    if (c >= N) return;
-    float s = red[threadIdx.x];
+    const int c = threadIdx.x % C, s = threadIdx.x / C;
+    if (s < S) {
+        float v = red[s * (TY / S) * C + c];
 #pragma unroll
-    for (int i = 1; i < TY; ++i) s += red[i * TX * 4 + threadIdx.x];
-    out[c] = s;
+        for (int i = 1; i < TY / S; ++i) v += red[(s * (TY / S) + i) * C + c];
+        red2[s * C + c] = v;
+    }
+    __syncthreads();
+    const int64_t n = (int64_t)C * blockIdx.x + threadIdx.x;
+    if (threadIdx.x >= C || n >= N) return;
+    float v = red2[threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < S; ++i) v += red2[i * C + threadIdx.x];
+    out[n] = v;
 }
 
 // Zeros (the column sums of no rows; a fill that a graph may capture).

@@ -185,7 +185,7 @@ hipError_t launch_col_sum(const float *part, int parts, int N, float *out, hipSt
     int n = parts, w = N;
     void *list[] = {&p, &n, &w, &out};
     return hipLaunchKernel(reinterpret_cast<const void *>(&sgemm::col_sum_kernel),
-                           dim3((unsigned)sgemm::ceil_div_ll(N, 32)), dim3(256), list, 0, stream);
+                           dim3((unsigned)sgemm::ceil_div_ll(N, 32)), dim3(sgemm::kColSumThreads), list, 0, stream);
 }
 
 hipError_t launch_zero(float *p, int n, hipStream_t stream)
@@ -212,15 +212,23 @@ hipError_t run_cols(sgemm::ColArgs a, float *out, float *parts, hipStream_t stre
 
 // ---- the norm's gradient --------------------------------------------------------------------
 
-// Workgroups of the one-pass form: each adds up dw over its rows, so more of
-// them mean more sums to add at the end.
-constexpr long long kRowGradWgs = 1024;
+// Workgroups of the one-pass form with a weight gradient.  Each adds up dw over
+// its own rows, and its D sums are written and read once more: four rows or
+// more each (times the four a workgroup of short rows holds at once) keep that
+// to an eighth of the traffic, but for at least 256 workgroups where the rows
+// allow, and at most 1024, which fill the chip.
+long long row_grad_wgs(const RowForm &f, int rows)
+{
+    const long long at_once = f.nt >= 256 ? 1 : 256 / f.nt;
+    const long long n = sgemm::ceil_div_ll(rows, 4 * at_once);
+    return n < 256 ? 256 : n < 1024 ? n : 1024;
+}
 
 // Floats of workspace the weight gradient needs, and the parts they hold.
 size_t row_grad_bytes(int rows, int D)
 {
     const RowForm f = row_form(D);
-    if (f.v > 0) return parts_bytes(row_grid(f, rows, kRowGradWgs), D);
+    if (f.v > 0) return parts_bytes(row_grid(f, rows, row_grad_wgs(f, rows)), D);
     // r of every row (16-byte padded), then the column pass's sums
     return (((size_t)rows + 3) & ~(size_t)3) * 4u + parts_bytes(col_plan(rows, D).chunks, D);
 }
@@ -262,7 +270,7 @@ hipError_t run_row_grad(int rows, int D, const float *dY, int ldy, const float *
     a.rows = rows;
     a.D = D;
     a.eps = eps;
-    const unsigned grid = row_grid(f, rows, dw && f.v > 0 ? kRowGradWgs : 0);
+    const unsigned grid = row_grid(f, rows, dw && f.v > 0 ? row_grad_wgs(f, rows) : 0);
     float *fws = static_cast<float *>(ws);
     if (dw && f.v > 0) a.dw = grid > 1 ? fws : dw;
     if (dw && f.v == 0) a.inv_rms = fws;
