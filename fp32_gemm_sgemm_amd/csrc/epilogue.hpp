@@ -78,6 +78,7 @@ constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 // a = 10.5 the exponential is 0 in float32.
 __device__ __forceinline__ void gelu_terms(float z, float &phi_cdf, float &gauss)
 {
+#pragma clang fp contract(off)  // s is the rounded square wherever it is used
     const float a = fminf(fabsf(z) * kSqrtHalf, 10.5f);
     const float s = a * a;
     gauss = expf(-s) * (1.0f - __builtin_fmaf(a, a, -s));

@@ -33,6 +33,17 @@ __device__ __forceinline__ uint32_t pack_e4m3(const float (&v)[4])
     return (uint32_t)p;
 }
 
+// s * w * (f_hi + f_lo), rounded once: with the parts that the products'
+// roundings drop (so no product may be fused into a later sum).
+__device__ __forceinline__ float code_value(float s, float w, float f_hi, float f_lo)
+{
+#pragma clang fp contract(off)
+    const float p = s * w;
+    const float p_lo = __builtin_fmaf(s, w, -p);
+    const float v = p * f_hi;
+    return v + (__builtin_fmaf(p, f_hi, -v) + __builtin_fmaf(p, f_lo, p_lo * f_hi));
+}
+
 // Codes of the values at columns below D.
 __device__ __forceinline__ void store_codes(unsigned char *p, int col, int D, const float (&v)[4])
 {
@@ -46,12 +57,16 @@ __device__ __forceinline__ void store_codes(unsigned char *p, int col, int D, co
     }
 }
 
+template <int NT> struct RowRed {
+    double a[NT / 64];
+    float b[NT / 64];
+};
+
 // Sums (and one maximum) over the NT threads that share a row.  A workgroup
 // that reduces once per row alternates between two halves of `red` (`turn`),
 // so one barrier a row is enough: the half is written again two rows later.
-template <int NT>
-__device__ __forceinline__ void row_reduce(float &a, float &b, bool b_is_max, float (*red)[2][NT / 64],
-                                           int turn)
+template <int NT, typename TA>
+__device__ __forceinline__ void row_reduce(TA &a, float &b, bool b_is_max, RowRed<NT> *red, int turn)
 {
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -62,26 +77,26 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, bool b_is_max, fl
     if constexpr (NT > 64) {
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) {
-            red[turn][0][wave] = a;
-            red[turn][1][wave] = b;
+            red[turn].a[wave] = a;
+            red[turn].b[wave] = b;
         }
         __syncthreads();
-        a = red[turn][0][0];
-        b = red[turn][1][0];
+        a = (TA)red[turn].a[0];
+        b = red[turn].b[0];
 #pragma unroll
         for (int w = 1; w < NT / 64; ++w) {
-            a += red[turn][0][w];
-            b = b_is_max ? fmaxf(b, red[turn][1][w]) : b + red[turn][1][w];
+            a += (TA)red[turn].a[w];
+            b = b_is_max ? fmaxf(b, red[turn].b[w]) : b + red[turn].b[w];
         }
     }
 }
 
 // LDS race check build: the half that the next row will write is set to NaN
 // after the barrier that ends its last use.
-template <int NT> __device__ __forceinline__ void row_poison(float (*red)[2][NT / 64], int turn)
+template <int NT> __device__ __forceinline__ void row_poison(RowRed<NT> *red, int turn)
 {
     if constexpr (kLdsPoison && NT > 64) {
-        if (threadIdx.x < 2 * (NT / 64)) lds_poison(&red[turn][0][0] + threadIdx.x, 1);
+        if (threadIdx.x < sizeof(RowRed<NT>) / 4) lds_poison(reinterpret_cast<float *>(&red[turn]) + threadIdx.x, 1);
         lds_poison_done();
         __syncthreads();
     }
@@ -102,7 +117,13 @@ constexpr int kRowCached = 16384;
 
 // Y = (S * w) * r, S = X + R, r = 1 / sqrt(mean(S^2) + eps) (NORM; else Y = X),
 // to float32 or (Q8) to e4m3 codes with the row's scale.  As rounding keeps
-// order, max|Y| is max|S * w| * r, so the statistics need one reduction.
+// order, max|Y| is max|S * w| * r, so the statistics need one reduction.  A
+// thread adds its few squares in float32, the threads' sums are added in
+// float64 (a few operations a row), and a code's value is the product S w r /
+// scale with the unrounded scale, carried in two float32 parts: next to the
+// border of two codes it goes the way the formula says, but for S's own
+// rounding (of the codes of 8192 x 8192 random rows none differs from the
+// 64-bit formula's; 34 do with the factor in float32).
 //
 // NT threads share a row, V groups of 4 values each (D <= 4 NT V); V == 0 is the
 // form for any D, which reads the row twice.  A workgroup has max(NT, 256)
@@ -112,8 +133,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_kernel(RowArgs a)
 {
     constexpr int RPB = NT >= 256 ? 1 : 256 / NT;  // rows a workgroup holds at once
     static_assert(RPB == 1 || NT == 64, "a row is one wave's or one workgroup's");
-    __shared__ float red_store[RPB == 1 ? 2 : 1][2][NT / 64];
-    float (*red)[2][NT / 64] = red_store;
+    __shared__ RowRed<NT> red[RPB == 1 ? 2 : 1];
     const int t = RPB == 1 ? threadIdx.x : threadIdx.x & 63;
     const int sub = RPB == 1 ? 0 : threadIdx.x >> 6;
     const int D = a.D;
@@ -124,7 +144,10 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_kernel(RowArgs a)
         float *so = a.S ? a.S + row * a.lds : nullptr;
         row_poison<NT>(red, turn);
         float sum = 0.0f, big = 0.0f;
-        float inv_rms = 1.0f, scale = 0.0f, inv_scale = 0.0f;
+        float inv_rms = 1.0f;
+        // S * w to its code's value: a factor in two parts, and a power of two
+        // for a row so small that the factor alone would overflow
+        float f_hi = 0.0f, f_lo = 0.0f, f_exp = 1.0f;
 
         // S of one group (masked to D), stored when wanted
         auto load_s = [&](int col, float (&s)[4]) {
@@ -146,31 +169,32 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_kernel(RowArgs a)
             }
         };
         auto finish_stats = [&]() {
-            row_reduce<NT>(sum, big, true, red, turn);
-            if (NORM) inv_rms = 1.0f / sqrtf(sum / (float)D + a.eps);
+            double total = sum;
+            row_reduce<NT>(total, big, true, red, turn);
+            const double r = NORM ? 1.0 / sqrt(total / D + a.eps) : 1.0;
+            inv_rms = (float)r;
             if (Q8) {
-                scale = fmaxf((NORM ? big * inv_rms : big) / kE4m3Max, kE4m3MinScale);
-                inv_scale = 1.0f / scale;
-                if (t == 0) a.scale[row] = scale;
+                const double scale = fmax(big * r / kE4m3Max, (double)kE4m3MinScale);
+                double f = r / scale;
+                if (f > 1e38) {
+                    f *= 0x1p-120;
+                    f_exp = 0x1p120f;
+                }
+                f_hi = (float)f;
+                f_lo = (float)(f - f_hi);
+                if (t == 0) a.scale[row] = (float)scale;
             }
         };
         auto write = [&](int col, const float (&s)[4]) {
-            float y[4] = {s[0], s[1], s[2], s[3]};
-            if (NORM && a.w) {
-                float w[4];
-                load_cols<4>(a.w + col, col, D, w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= w[j];
-            }
-            if (NORM) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= inv_rms;
-            }
+            float y[4], w[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+            if (NORM && a.w) load_cols<4>(a.w + col, col, D, w);
             if (Q8) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= inv_scale;
+                for (int j = 0; j < 4; ++j) y[j] = code_value(s[j], NORM ? w[j] : 1.0f, f_hi, f_lo) * f_exp;
                 store_codes(a.Q + row * a.ldq + col, col, D, y);
             } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = s[j] * w[j] * inv_rms;
                 store_row<4>(a.Y + row * a.ldy + col, col, D, y, 1.0f, 0.0f);
             }
         };
@@ -239,8 +263,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) row_grad_kernel(RowGradAr
     constexpr int RPB = NT >= 256 ? 1 : 256 / NT;
     constexpr int VS = V > 0 ? V : 1;
     static_assert(RPB == 1 || NT == 64, "a row is one wave's or one workgroup's");
-    __shared__ float red_store[RPB == 1 ? 2 : 1][2][NT / 64];
-    float (*red)[2][NT / 64] = red_store;
+    __shared__ RowRed<NT> red[RPB == 1 ? 2 : 1];
     // short rows: the waves' dw sums meet here
     __shared__ __attribute__((aligned(16))) float dw_lds[RPB == 1 ? 4 : (RPB - 1) * 256 * VS];
     const int t = RPB == 1 ? threadIdx.x : threadIdx.x & 63;

@@ -52,6 +52,22 @@ RowForm row_form(int D)
     return {1024, 0};
 }
 
+// The form of a norm or quantisation.  With rows enough to fill the chip, long
+// rows go to workgroups of 512: four of them share a compute unit and one's
+// arithmetic overlaps another's memory (8192 x 8192: quantize 74 to 61 us, 8-bit
+// norm with residual 182 to 166, norm 108 to 99, norm with residual 194 to 200;
+// 2048 x 5120: 16 to 13, 36 to 31, 19 to 18, 37 to 34).  Past 8192 values that
+// pays only where no residual is read too (4096 x 16384: quantize 77 to 69, norm
+// with residual 208 to 214).  Few rows wait for one workgroup's latency, which
+// more threads shorten (1 x 8192, norm with residual: 5.0 to 4.5 us).
+RowForm row_form_forward(int D, int rows, bool residual)
+{
+    constexpr int kRowsToFill = 1024;
+    if (rows >= kRowsToFill && D > 4096 && D <= 8192) return {512, 4};
+    if (rows >= kRowsToFill && D > 8192 && D <= sgemm::kRowCached && !residual) return {512, 8};
+    return row_form(D);
+}
+
 // Workgroups of a row operator: one per row (or four short ones), as many as
 // the dispatch packet counts; the kernels loop over the rest.
 unsigned row_grid(const RowForm &f, int rows, long long most)
@@ -80,6 +96,10 @@ template <bool NORM, bool Q8> const void *row_kernel_for(const RowForm &f)
     if (f.nt == 256) {
         if (f.v == 2) return reinterpret_cast<const void *>(&row_kernel<256, 2, NORM, Q8>);
         return reinterpret_cast<const void *>(&row_kernel<256, 4, NORM, Q8>);
+    }
+    if (f.nt == 512) {
+        if (f.v == 4) return reinterpret_cast<const void *>(&row_kernel<512, 4, NORM, Q8>);
+        return reinterpret_cast<const void *>(&row_kernel<512, 8, NORM, Q8>);
     }
     if (f.v == 2) return reinterpret_cast<const void *>(&row_kernel<1024, 2, NORM, Q8>);
     if (f.v == 4) return reinterpret_cast<const void *>(&row_kernel<1024, 4, NORM, Q8>);
@@ -145,7 +165,7 @@ hipError_t run_row(bool norm, bool q8, int rows, int D, const float *X, int ldx,
     a.rows = rows;
     a.D = D;
     a.eps = eps;
-    const RowForm f = row_form(D);
+    const RowForm f = row_form_forward(D, rows, R != nullptr);
     const void *fn = norm ? (q8 ? row_kernel_for<true, true>(f) : row_kernel_for<true, false>(f))
                           : row_kernel_for<false, true>(f);
     return launch1(fn, dim3(row_grid(f, rows, 0)), f.nt > 256 ? f.nt : 256, &a, stream);

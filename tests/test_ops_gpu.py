@@ -376,6 +376,44 @@ def test_rmsnorm(D, residual):
         assert torch.equal(s8, s)
 
 
+@pytest.mark.parametrize("D", [4100, 8192, 8200, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_many_long_rows(D, residual):
+    """The forms that long rows take once there are many of them: the same
+    values as the first rows alone, within the bounds, to the last row."""
+    rows = 1030
+    note(f"rmsnorm {rows}x{D} residual={residual}")
+    x, w = normal(rows, D, seed=1), (1 + 0.2 * normal(D, seed=2)).astype(np.float32)
+    R = normal(rows, D, seed=3) if residual else None
+    Y, S, ty, rho = ref.rmsnorm(x.astype(np.float64), w.astype(np.float64), 1e-6,
+                                None if R is None else R.astype(np.float64))
+    out, ok = guarded(rows, D)
+    y, s = sg.rmsnorm(dev(x, 1), dev(w), residual=None if R is None else dev(R), out=out)
+    torch.cuda.synchronize()
+    ref.within(f64(out), Y, ty)
+    ok()
+    q, scale, _ = sg.rmsnorm_e4m3(dev(x, 1), dev(w), residual=None if R is None else dev(R))
+    torch.cuda.synchronize()
+    ref.check_codes(f64(q.float()), f64(scale), Y, ty, rho + 8 * ref.U)
+    q, scale = sg.quantize_e4m3(dev(x, 3))
+    torch.cuda.synchronize()
+    x64 = x.astype(np.float64)
+    ref.check_codes(f64(q.float()), f64(scale), x64, np.zeros_like(x64), 0.0)
+
+
+def test_quantize_codes_are_the_formulas():
+    """Every code is the rounding of x / (max|x| / 448) in 64 bits: values are
+    carried to float32 with one rounding, so only one that lies within half a
+    unit of float32's last place of the border of two codes could differ."""
+    for rows, D in ((3, 700), (300, 4096), (1500, 5000)):
+        x = normal(rows, D, seed=D)
+        q, _ = sg.quantize_e4m3(dev(x))
+        v = x.astype(np.float64) / (np.abs(x.astype(np.float64)).max(1, keepdims=True) / 448)
+        got = f64(q.float())
+        step = np.maximum(2.0 ** (np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -6))) - 3), 2.0 ** -9)
+        assert np.all(np.abs(got - v) <= step / 2 + ref.U * np.abs(v))
+
+
 def test_rmsnorm_in_place():
     """The residual stream updated in place; y over x."""
     for D in (300, 4096, 20000):
@@ -407,6 +445,12 @@ def test_rmsnorm_special_rows():
         q, scale = f64(q.float()), f64(scale)
         assert np.isfinite(q[[0, 1, 4]]).all() and (q[1] == 0).all() and scale[1] == 2.0 ** -126
         assert np.isnan(q[2, 5]) and (np.delete(q[2], 5) == 0).all() and np.isnan(q[3]).all()
+        # a row below the smallest scale: its codes are Y / 2^-126
+        tiny = np.full((1, D), 1e-41, np.float32)
+        tiny[0, 1:] = 0
+        q, scale, _ = sg.rmsnorm_e4m3(dev(tiny), eps=1e-6)
+        want = float(np.float64(tiny[0, 0]) * 1e3 / 2.0 ** -126)
+        assert scale.item() == 2.0 ** -126 and abs(q[0, 0].float().item() - want) <= want / 16
         y, _ = sg.rmsnorm(dev(x), eps=0.0)
         assert np.isnan(f64(y)[1]).all() and np.isfinite(f64(y)[0]).all()
 
