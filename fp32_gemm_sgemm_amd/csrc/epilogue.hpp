@@ -15,8 +15,8 @@
 //              (1 + tanh u) / 2 = sigma(2u); c = sqrt(2/pi), a = 0.044715
 //                                          s + 2c z s (1 - s) (1 + 3 a z^2)
 //   silu       z sigma(z)                                s (1 + z (1 - s))
-// Everything is float32, with the math library's expf and the hardware's
-// reciprocal (about one unit in the last place each).  Phi is computed from
+// Everything is float32, on the hardware's 2^x and reciprocal (about one unit
+// in the last place each).  Phi is computed from
 // its own polynomial (gelu_terms): without branches, and with its relative
 // accuracy kept in the lower tail, where (1 + erf) / 2 cancels.
 #pragma once
@@ -50,11 +50,28 @@ __device__ __forceinline__ float load_global(const float *p)
     return *(global_float *)(uintptr_t)p;
 }
 
+// exp(-t) for t >= 0 (infinity and NaN give 0), within about 2 units in the last
+// place down to 2^-126 and 0 below: the hardware's 2^x of t log2(e) carried in
+// two parts.  (The math library's expf takes three times the instructions for
+// the arguments that cannot occur here; a 256 x 256 tile's epilogue is bound by
+// them.)
+__device__ __forceinline__ float exp_neg(float t)
+{
+#pragma clang fp contract(off)
+    constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596303e-8f, kLn2 = 0.693147181f;
+    const float x = fminf(t, 200.0f);
+    const float hi = x * kLog2e;
+    const float lo = __builtin_fmaf(x, kLog2eLow, __builtin_fmaf(x, kLog2e, -hi));
+    const float r = __builtin_amdgcn_exp2f(-hi);
+    return __builtin_fmaf(r, -kLn2 * lo, r);
+}
+
 // sigma(t) and 1 - sigma(t), each with its own relative accuracy: from
-// exp(-|t|), which neither overflows nor cancels.  NaN passes.
+// exp(-|t|), which neither overflows nor cancels.  (NaN gives 1 and 0: what they
+// are multiplied by is NaN then.)
 __device__ __forceinline__ float sigmoid_f32(float t, float &rest)
 {
-    const float e = expf(-fabsf(t));
+    const float e = exp_neg(fabsf(t));
     const float q = __builtin_amdgcn_rcpf(1.0f + e), p = e * q;
     rest = t < 0.0f ? q : p;
     return t < 0.0f ? p : q;
@@ -81,7 +98,7 @@ __device__ __forceinline__ void gelu_terms(float z, float &phi_cdf, float &gauss
 #pragma clang fp contract(off)  // s is the rounded square wherever it is used
     const float a = fminf(fabsf(z) * kSqrtHalf, 10.5f);
     const float s = a * a;
-    gauss = expf(-s) * (1.0f - __builtin_fmaf(a, a, -s));
+    gauss = exp_neg(s) * (1.0f - __builtin_fmaf(a, a, -s));
     const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.5f, a, 1.0f));
     float p = -0.05921298f;
     p = __builtin_fmaf(p, t, 0.28527875f);
@@ -238,15 +255,21 @@ template <bool SLOPE> __device__ __forceinline__ void epi_map(int act, f32x4 &v)
 // `grad_pre` and the residual is 16 bytes per lane along a row: a lane keeps
 // its four columns (bias and column scales are read once) and walks down the
 // rows.  Loads and stores retire in order on one counter, so a load issued
-// after a store waits for it: reads are issued B rows at a time before the
-// stores of those rows, and nothing is read in between (with one row at a time
+// after a store waits for it: reads are issued B steps at a time before the
+// stores of those rows, and nothing is read in between (with one step at a time
 // a 2048 x 2048 x 1024 product of 8-bit operands spent 13 of its 29 us waiting
 // for its own stores).  SCALES: row and column scales may be given.
+//
+// What it costs, on the float32 256x256 tile at 2048 x 8192 x 2048 (one tile per
+// compute unit, so nothing hides it): the product alone 464 us, with bias 464,
+// with gelu and the stored pre-activation 477, with a residual 473, with gelu's
+// slope 479; the same product and the passes over its output one after the
+// other take 603.
 template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
     static constexpr int QR = WT / 4;     // 16-byte groups per row
     static constexpr int STEP = 64 / QR;  // rows a wave covers at once
     static constexpr int STEPS = R / STEP;
-    static constexpr int B = STEPS < 8 ? STEPS : 8;  // steps whose reads are in flight together
+    static constexpr int B = STEPS < 8 ? STEPS : SCALES ? 8 : 4;  // steps whose reads are in flight together
     static constexpr int RSTEP = RS * STEP;
     static_assert(64 % QR == 0 && R % STEP == 0 && STEPS % B == 0 && R <= 64, "whole wave steps");
 
