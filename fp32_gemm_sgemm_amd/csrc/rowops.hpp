@@ -417,7 +417,12 @@ struct ColArgs {
 };
 
 // A workgroup covers 4 TX columns of one chunk of rows (blockIdx.y), TX = 64
-// or 16 lanes along the columns and 256 / TX rows at a time.
+// or 16 lanes along the columns and 256 / TX rows at a time.  A lane reads
+// its next row before it works on the present one and stores it: loads and
+// stores retire in order on one counter, so a row read after a store would wait
+// for that store (512 x 8192 with gelu: 14.1 us without, 13.5 so; two or four
+// rows at once are 14.9 and 15.1, as they leave less of the slope's arithmetic
+// to overlap).
 template <int KIND, int TX>
 __global__ void __launch_bounds__(256) col_kernel(ColArgs a)
 {
@@ -429,29 +434,47 @@ __global__ void __launch_bounds__(256) col_kernel(ColArgs a)
     const int col = in ? (int)col64 : 0;
     const int64_t m0 = (int64_t)blockIdx.y * a.rows_per_chunk;
     const int64_t m1 = m0 + a.rows_per_chunk < a.M ? m0 + a.rows_per_chunk : a.M;
+    constexpr bool NORM = KIND == kColNorm;
+    const bool reads_z = NORM || a.act != SGEMM_ACT_NONE;
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (in) {
-#pragma unroll 4
-        for (int64_t m = m0 + ty; m < m1; m += TY) {
-            float y[4];
-            load_cols<4>(a.Y + m * a.ldy + col, col, a.N, y);
-            if constexpr (KIND == kColNorm) {
-                float s[4];
-                load_cols<4>(a.Z + m * a.ldz + col, col, a.N, s);
-                const float r = a.r[m];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] *= s[j] * r;
+        typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+        const bool whole = col + 3 < a.N;
+        f32x4 y = {}, z = {};
+        float r = 0.0f;
+        auto read = [&](int64_t m) {
+            const float *const py = a.Y + m * a.ldy + col, *const pz = a.Z + m * a.ldz + col;
+            if (whole) {
+                y = *reinterpret_cast<const f32x4u *>(py);
+                if (reads_z) z = *reinterpret_cast<const f32x4u *>(pz);
             } else {
-                if (a.act != SGEMM_ACT_NONE) {
-                    float z[4];
-                    load_cols<4>(a.Z + m * a.ldz + col, col, a.N, z);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] *= act_slope(a.act, z[j]);
+                for (int j = 0; j < 4; ++j) {
+                    y[j] = col + j < a.N ? py[j] : 0.0f;
+                    if (reads_z) z[j] = col + j < a.N ? pz[j] : 0.0f;
                 }
-                if (a.out) store_row<4>(a.out + m * a.ldo + col, col, a.N, y, 1.0f, 0.0f);
             }
+            if constexpr (NORM) r = a.r[m];
+        };
+        int64_t m = m0 + ty;
+        if (m < m1) read(m);
+        while (m < m1) {
+            f32x4 x = y, s = z;
+            const float f = r;
+            const int64_t at = m;
+            m += TY;
+            if (m < m1) read(m);
+            if constexpr (NORM) {
+                x *= s * f;
+            } else if (reads_z) {
+                epi_map<true>(a.act, s);
+                x *= s;
+            }
+            float v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] += y[j];
+            for (int j = 0; j < 4; ++j) sum[j] += v[j] = x[j];
+            if constexpr (!NORM)
+                if (a.out) store_row<4>(a.out + at * a.ldo + col, col, a.N, v, 1.0f, 0.0f);
         }
     }
     if (!a.part) return;  // (the same for every thread)
