@@ -455,7 +455,9 @@ template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_ski
         lds_poison_done();
         __syncthreads();
     }
-    for (int n0 = 16 * (int)blockIdx.x; n0 < N; n0 += 16 * (int)gridDim.x) {
+    // (64 bits: the last workgroup's next column can pass 2^31)
+    for (int64_t c0 = 16 * (int64_t)blockIdx.x; c0 < N; c0 += 16 * (int64_t)gridDim.x) {
+        const int n0 = (int)c0;
         const unsigned char *b = reinterpret_cast<const unsigned char *>(g.B) + min(n0 + lr, N - 1) * g.ld_b;
         const unsigned char *a[RM];
 #pragma unroll

@@ -64,15 +64,16 @@ constexpr double kE4m3StreamBytesPerNs = 6000.0;
 constexpr int kE4m3MaxLdDirect = 1 << 23;
 constexpr int kE4m3SplitAlign = 128;  // codes: whole slices, and 16-byte aligned starts
 
+constexpr int kE4m3None = kE4m3VariantCount;  // more tiles than a grid counts
 struct E4m3Plan {
-    int variant;  // a tile, or the streaming kernel -1 - i
+    int variant;  // a tile, or the streaming kernel -1 - i, or kE4m3None
     int splits, k_chunk;
     long long workspace_bytes;
 };
 
 E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws)
 {
-    E4m3Plan best = {-1, 1, K > 0 ? K : 1, 0};
+    E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0};
     double best_t = -1.0;
     for (int i = 0; i < kE4m3SkinnyCount; ++i) {
         const E4m3Skinny &s = kE4m3Skinny[i];
@@ -170,6 +171,7 @@ hipError_t run_e4m3(int M, int N, int K, const void *A, int lda, const float *sc
     const bool aligned = e4m3_aligned(A, lda, B, ldb);
     const E4m3Plan plan = e4m3_plan(M, N, K, cus, aligned,
                                     ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)ws_bytes);
+    if (plan.variant == kE4m3None) return hipErrorInvalidValue;
     sgemm::E4m3Args g = {};
     g.A = static_cast<const float *>(A);
     g.B = static_cast<const float *>(B);

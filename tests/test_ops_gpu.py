@@ -637,6 +637,70 @@ def test_gemm_e4m3_nan_codes():
         assert np.array_equal(np.isnan(y), bad)
 
 
+# ---- far apart ---------------------------------------------------------------------------------------
+
+def test_rows_further_apart_than_32_bits():
+    """Row strides of 2^30 floats: the third row starts 2^33 bytes in.  Inputs
+    and outputs of the row operators, and the epilogue's tensors."""
+    M, D, ld = 3, 700, 1 << 30
+    big = [torch.empty(2 * ld + D + 4, device="cuda") for _ in range(4)]
+
+    def far(i, x=None):
+        v = big[i][1:].as_strided((M, D), (ld, 1), 1)
+        if x is not None:
+            v.copy_(x)
+        return v
+    x, r, w = (dev(normal(*s, seed=i)) for i, s in enumerate(((M, D), (M, D), (D,))))
+    y, s = sg.rmsnorm(x, w, residual=r)
+    Y, S = sg.rmsnorm(far(0, x), w, residual=far(1, r), sum_out=far(2), out=far(3))
+    assert torch.equal(Y, y) and torch.equal(S, s)
+    q, c, _ = sg.rmsnorm_e4m3(x, w, residual=r)
+    Q, C, S = sg.rmsnorm_e4m3(far(0, x), w, residual=far(1, r), sum_out=far(2))
+    assert torch.equal(Q.float(), q.float()) and torch.equal(C, c) and torch.equal(S, s)
+    d, dw = sg.rmsnorm_backward(y, s, w, dsum=r)
+    Dx, Dw = sg.rmsnorm_backward(far(0, y), far(1, s), w, dsum=far(2, r), out=far(3))
+    assert torch.equal(Dx, d) and torch.equal(Dw, dw)
+    z, b = sg.activation_grad(x, r, "gelu")
+    Z, B = sg.activation_grad(far(0, x), far(1, r), "gelu", out=far(2))
+    assert torch.equal(Z, z) and torch.equal(B, b)
+    K = 40
+    A, Bm = normal(M, K, seed=5), normal(K, D, seed=6)
+    pre, out = far(2), far(3)
+    sg.sgemm_epilogue(dev(A), dev(Bm), activation="silu", residual=far(1, r), pre=pre, out=out)
+    Yr, Zr, ty, tz = ref.product(A.astype(np.float64), Bm.astype(np.float64), K, 1.0, None, "silu", f64(r))
+    ref.within(f64(pre), Zr, tz, "pre")
+    ref.within(f64(out), Yr, ty, "out")
+    sg.sgemm_epilogue(dev(A), dev(Bm), activation="silu", grad_pre=far(0, x), out=out)
+    Yr, _, ty, _ = ref.product(A.astype(np.float64), Bm.astype(np.float64), K, 1.0, None, "silu", None, f64(x))
+    ref.within(f64(out), Yr, ty, "gradient")
+
+
+@pytest.mark.parametrize("M", [5, 70])
+def test_codes_further_apart_than_32_bits(M):
+    """8-bit rows whose last starts past 2^32 bytes, both operands in turn: the
+    kernel of few rows and the tiles."""
+    N, K = 70, 300
+    ld = (1 << 32) // (M - 1) + 5
+    (a, A), (b, B) = codes(M, K, 1), codes(N, K, 2)
+    buf = torch.empty((M - 1) * ld + K, dtype=torch.uint8, device="cuda")
+    far = buf.as_strided((M, K), (ld, 1))
+    far.copy_(a.view(torch.uint8))
+    far = far.view(torch.float8_e4m3fn)
+    Y, _, ty, _ = ref.product(A, B.T, K)
+    ref.within(f64(sg.gemm_e4m3(far, None, b, None)), Y, ty)
+    ref.within(f64(sg.gemm_e4m3(b, None, far, None)).T, Y, ty)
+
+
+def test_gemm_e4m3_more_columns_than_one_grid():
+    """So many outputs that a workgroup's next column passes 2^31."""
+    N = 1_620_000_000
+    b = torch.randint(0, 0x78, (N, 1), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    one = torch.ones(1, 1, device="cuda").to(torch.float8_e4m3fn)
+    y = sg.gemm_e4m3(one, None, b, None)
+    for i in range(0, N, 1 << 28):
+        assert torch.equal(y[0, i:i + (1 << 28)], b[i:i + (1 << 28), 0].float())
+
+
 # ---- together ---------------------------------------------------------------------------------------
 
 def test_training_block_together():
