@@ -7,10 +7,11 @@
 // row operators therefore make one pass: a row is held in the registers of one
 // wave or one workgroup (up to kRowCached values), its statistics are reduced
 // across them, and what is written comes from the registers.  Longer rows are
-// read a second time (from L2, mostly).  Sums and statistics are float32 and
-// added in a fixed order: per thread, then a butterfly of lane shuffles, then
-// the waves in order through LDS; column sums per workgroup over a fixed set of
-// rows, then over the workgroups in order by a second kernel.
+// read a second time (from L2, mostly).  Sums are added in a fixed order: per
+// thread, then a butterfly of lane shuffles, then the waves in order through
+// LDS; column sums per workgroup over a fixed set of rows, then over the
+// workgroups in order by a second kernel.  They are float32, but for the forward
+// norm's across threads (float64, see row_kernel).
 #pragma once
 
 #include "common.hpp"

@@ -15,6 +15,7 @@ from .binding import (ACTIVATIONS, SgemmEpilogue, _check, load, sgemm, sgemm_f32
                       sgemm_f32_workspace_size)
 
 E4M3_MAX = 448.0
+_MAX_DIM = 2**31 - 1 - 1024  # largest size, row stride or batch the C ABI takes
 _torch_module = None
 
 
@@ -82,6 +83,8 @@ def _rows(t, name, dtype=None):
         ld = cols
     elif ld < cols:
         raise ValueError(f"{name}'s rows must not overlap (row stride {ld}, {cols} columns)")
+    if rows > _MAX_DIM or cols > _MAX_DIM or ld > _MAX_DIM:
+        raise ValueError(f"{name}'s sizes and row stride must not pass {_MAX_DIM}")
     return rows, cols, ld if ld > 0 else 1
 
 
@@ -132,6 +135,8 @@ def _supplied(workspace, device):
     """(address, bytes) of a caller's workspace tensor."""
     if workspace.device != device:
         raise ValueError("workspace must be a device tensor on the operands' GPU")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -142,6 +147,8 @@ def _batch_view(t, name):
     if t.dim() != 3:
         raise ValueError(f"{name} must be 2-D or 3-D")
     n = t.shape[0]
+    if n > _MAX_DIM:
+        raise ValueError(f"{name} must not have more than {_MAX_DIM} batch entries")
     return (n, *_rows(t[0] if n else t.new_empty(t.shape[1:]), name), t.stride(0) if n > 1 else 0)
 
 
@@ -350,7 +357,7 @@ def _norm_inputs(x, weight, residual, sum_out, device):
 def rmsnorm(x, weight=None, *, eps=1e-6, residual=None, sum_out=None, out=None, stream=None):
     """(y, s): s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight, per row.
 
-    Without `residual`, s is x itself.  `sum_out` receives s (it may be `x` or
+    Without `residual`, s is x itself (and lost where `out` is x).  `sum_out` receives s (it may be `x` or
     `residual`, which then holds the residual stream updated in place).
     """
     device = _gpu_of(x, "x")

@@ -135,7 +135,8 @@ int sgemm_f32_activation_grad_workspace(int M, int N, size_t *bytes);
  *   Y       rows x D; it may be X's, R's memory when S is not.
  *   eps     >= 0, finite.  A row of zeros with eps == 0 gives NaN (0 / 0).
  * D >= 1, rows >= 0, both <= INT_MAX - 1024; every ld >= D.  Squares are
- * float32 (|S| above 1.8e19 overflows), their sum across threads float64.
+ * float32 (|S| above 1.8e19 overflows), their sum across threads float64; S * w
+ * is formed in float32.
  */
 int sgemm_rmsnorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr,
                       const float *w, float eps, float *S, int lds, float *Y, int ldy,

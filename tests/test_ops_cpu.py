@@ -230,6 +230,29 @@ def test_rows_that_overlap_are_refused():
         binding._row_major_view(torch.zeros(8, 4).t(), "A")
 
 
+def test_sizes_past_the_abi_are_refused():
+    """Sizes and strides that an int does not hold must not be cut to one that
+    it does (tensors without memory: only their shapes are read)."""
+    torch = pytest.importorskip("torch")
+    from fp32_gemm_sgemm_amd import ops
+    most = 2**31 - 1 - 1024
+
+    def meta(rows, cols, ld):
+        return torch.empty_strided((rows, cols), (ld, 1), device="meta")
+    assert ops._rows(meta(2, 8, most), "x") == (2, 8, most)
+    assert ops._rows(meta(most, 1, 1), "x") == (most, 1, 1)
+    for x in (meta(2, 8, most + 1), meta(2, 8, 2**32 + 8), meta(2**32, 1, 1), meta(1, 2**32 + 4, 1),
+              meta(2, 2**32 + 4, 2**33)):
+        with pytest.raises(ValueError, match="must not pass"):
+            ops._rows(x, "x")
+    with pytest.raises(ValueError, match="batch entries"):
+        ops._batch_view(torch.empty_strided((2**32 + 1, 2, 2), (0, 2, 1), device="meta"), "x")
+    x = torch.zeros(4)
+    assert ops._supplied(x, x.device) == (x.data_ptr(), 16)
+    with pytest.raises(ValueError, match="contiguous"):
+        ops._supplied(torch.zeros(1).expand(1 << 20), x.device)
+
+
 def test_host_tensors_and_types_are_refused():
     torch = pytest.importorskip("torch")
     x, q = torch.zeros(4, 8), torch.zeros(4, 8, dtype=torch.uint8).view(torch.float8_e4m3fn)

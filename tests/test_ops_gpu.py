@@ -312,6 +312,18 @@ def test_epilogue_backward(M, N, K, ta, tb):
     ref.within(f64(z), dY.astype(np.float64).sum(0), np.abs(dY).sum(0) * (M + 1) * ref.U + 1e-37)
 
 
+@pytest.mark.parametrize("M,N,K", [(0, 5, 7), (6, 0, 7), (6, 5, 0)])
+def test_epilogue_backward_of_nothing(M, N, K):
+    """An empty dimension: gradients of the operands' shapes, zeros where the
+    sum is empty."""
+    note(f"backward of nothing {M}x{N}x{K}")
+    g, pre = torch.ones(M, N, device="cuda"), torch.ones(M, N, device="cuda")
+    A, B = torch.ones(M, K, device="cuda"), torch.ones(K, N, device="cuda")
+    dA, dB, db = sg.sgemm_epilogue_backward(g, A, B, pre=pre, activation="relu", a_pre=A, a_activation="relu")
+    assert dA.shape == A.shape and dB.shape == B.shape and db.shape == (N,)
+    assert bool((dA == 0).all()) and bool((dB == 0).all()) and bool((db == M).all())
+
+
 @pytest.mark.parametrize("name", ref.ACTS)
 def test_gradients_against_differences(name):
     """Central differences of the 64-bit forward pass along random directions.
