@@ -11,7 +11,7 @@ on the stream it runs on, as torch does under `torch.cuda.stream(stream)`.
 """
 import ctypes
 
-from .binding import (ACTIVATIONS, SgemmEpilogue, _check, load, sgemm, sgemm_f32_cfg_geometry,
+from .binding import (ACTIVATIONS, SgemmEpilogue, _check, load, sgemm_f32_cfg_geometry,
                       sgemm_f32_workspace_size)
 
 E4M3_MAX = 448.0
@@ -304,35 +304,58 @@ def sgemm_epilogue_backward(grad, A, B, *, pre=None, activation=None, a_pre=None
                                            need=need, workspace=workspace)
     _same_gpu(device, A, "A")
     _same_gpu(device, B, "B")
-    ra, ca, _ = _rows(A, "A")
-    rb, cb, _ = _rows(B, "B")
+    ra, ca, lda = _rows(A, "A")
+    rb, cb, ldb = _rows(B, "B")
     M, K = (ca, ra) if transa else (ra, ca)
     K2, N = (cb, rb) if transb else (rb, cb)
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    _matrix(grad, M, N, device, "grad")
+    ldz = _matrix(grad, M, N, device, "grad")
     act, a_act = _activation(activation), _activation(a_activation)
+    below = None
     if a_act:
         if a_pre is None:
             raise ValueError("a_activation needs `a_pre`")
-        _matrix(a_pre, ra, ca, device, "a_pre")
+        ld = _matrix(a_pre, ra, ca, device, "a_pre")
+        below = SgemmEpilogue(activation=a_act, grad_pre=a_pre.data_ptr(), ld_grad_pre=ld)
     dz, dbias, dA, dB = grad, None, None, None
     products = "A" in need or "B" in need
     if "bias" in need or (act and products):
         dz, dbias = activation_grad(grad, pre, activation, out=None if act and products else False,
                                     dbias=None if "bias" in need else False)
-        dz = grad if dz is None else dz
+        dz, ldz = (grad, ldz) if dz is None else (dz, max(N, 1))
+    a, b, z = (A, lda), (B, ldb), (dz, ldz)
     if "A" in need:
-        X, Y, tx, ty = (B, dz, transb, True) if transa else (dz, B, False, not transb)
-        if a_act:
-            dA = sgemm_epilogue(X, Y, transa=tx, transb=ty, alpha=alpha, activation=a_activation, grad_pre=a_pre,
-                                workspace=workspace)
-        else:
-            dA = sgemm(X, Y, transa=tx, transb=ty, alpha=alpha, workspace=workspace)
+        x, y, tx, ty = (b, z, transb, True) if transa else (z, b, False, not transb)
+        dA = _product(x, tx, y, ty, ra, ca, N, alpha, workspace, device, below)
     if "B" in need:
-        X, Y, tx, ty = (dz, A, True, transa) if transb else (A, dz, not transa, False)
-        dB = sgemm(X, Y, transa=tx, transb=ty, alpha=alpha, workspace=workspace)
+        x, y, tx, ty = (z, a, True, transa) if transb else (a, z, not transa, False)
+        dB = _product(x, tx, y, ty, rb, cb, M, alpha, workspace, device)
     return dA, dB, dbias
+
+
+def _product(x, tx, y, ty, M, N, K, alpha, workspace, device, epilogue=None):
+    """alpha * op(X) @ op(Y) (M x N, inner size K) of checked (tensor, row
+    stride) pairs, through `epilogue` if given: sgemm()'s product without its
+    checks, which cost a small gradient 8 us a product."""
+    (X, ldx), (Y, ldy), tx, ty = x, y, 1 if tx else 0, 1 if ty else 0
+    out, ldo = _empty((M, N), device), max(N, 1)
+    ws, ws_ptr, ws_bytes = None, None, 0
+    if isinstance(workspace, _torch().Tensor):
+        ws_ptr, ws_bytes = _supplied(workspace, device)
+    elif workspace and M and N and K:
+        ws_bytes = sgemm_f32_workspace_size(tx, ty, M, N, K, ldx, ldy, ldo)
+        ws, ws_ptr = _scratch(ws_bytes, device)
+    where = "sgemm_f32_ex" if epilogue is None else "sgemm_f32_epilogue"
+    args = (tx, ty, M, N, K, float(alpha), X.data_ptr(), ldx, 0, Y.data_ptr(), ldy, 0)
+    to = (out.data_ptr(), ldo, 0, 1)
+    if epilogue is None:
+        code = load().sgemm_f32_ex(*args, 0.0, *to, ws_ptr, ws_bytes, _handle(device), None)
+    else:
+        code = load().sgemm_f32_epilogue(*args, *to, ctypes.byref(epilogue), ws_ptr, ws_bytes, _handle(device), None)
+    del ws
+    _check(code, where)
+    return out
 
 
 def _norm_inputs(x, weight, residual, sum_out, device):
