@@ -261,17 +261,20 @@ template <bool SLOPE> __device__ __forceinline__ void epi_map(int act, f32x4 &v)
 // for its own stores).  SCALES: row and column scales may be given.
 //
 // What it costs, on the float32 256x256 tile at 2048 x 8192 x 2048 (one tile per
-// compute unit, so nothing hides it): the product alone 464 us, with bias 464,
-// with gelu and the stored pre-activation 477, with a residual 473, with gelu's
+// compute unit, so nothing hides it): the product alone 462 us, with bias 462,
+// with gelu and the stored pre-activation 475, with a residual 472, with gelu's
 // slope 479; the same product and the passes over its output one after the
-// other take 603.
+// other take 606.  Tiles that reach past the last row or column run the same
+// steps with masks (1728 x 1292 x 494 with bias: 37.0 us, 39.1 when each step
+// waited for its own store; 8-bit 1000 x 1000 x 1000: 12.6 against 14.2).
 template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
     static constexpr int QR = WT / 4;     // 16-byte groups per row
     static constexpr int STEP = 64 / QR;  // rows a wave covers at once
     static constexpr int STEPS = R / STEP;
-    static constexpr int B = STEPS < 8 ? STEPS : SCALES ? 8 : 4;  // steps whose reads are in flight together
+    static constexpr int BF = STEPS < 8 ? STEPS : SCALES ? 8 : 4;  // steps whose reads are in flight together
+    static constexpr int BE = BF < 4 ? BF : BF / 2;                // and at an edge (more would take registers from the loop)
     static constexpr int RSTEP = RS * STEP;
-    static_assert(64 % QR == 0 && R % STEP == 0 && STEPS % B == 0 && R <= 64, "whole wave steps");
+    static_assert(64 % QR == 0 && R % STEP == 0 && STEPS % BF == 0 && STEPS % BE == 0 && R <= 64, "whole wave steps");
 
     const EpiGemmArgs &g;
     const int z, lane, col0;
@@ -284,9 +287,17 @@ template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
     {
         scale = f32x4{g.alpha, g.alpha, g.alpha, g.alpha};
         bias = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (col0 + WT > g.N) return;  // (the edge path reads its own)
-        if (SCALES && g.e.scale_b) scale = *reinterpret_cast<const f32x4u *>(g.e.scale_b + col());
-        if (g.e.bias) bias = *reinterpret_cast<const f32x4u *>(g.e.bias + z * g.e.batch_bias + col());
+        if (SCALES && g.e.scale_b) scale = columns(g.e.scale_b);
+        if (g.e.bias) bias = columns(g.e.bias + z * g.e.batch_bias);
+    }
+
+    // The lane's four columns of a row vector, zeros past N.
+    __device__ __forceinline__ f32x4 columns(const float *p) const
+    {
+        if (col0 + WT <= g.N) return *reinterpret_cast<const f32x4u *>(p + col());
+        float x[4];
+        load_cols<4>(p + col(), col(), g.N, x);
+        return f32x4{x[0], x[1], x[2], x[3]};
     }
 
     // The scale of the region's row `lane` (of R), to be read for all regions
@@ -299,31 +310,45 @@ template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
 
     __device__ __forceinline__ void store(float *lds, int row0, float row_scale) const
     {
+        if (col0 + WT > g.N || row0 + RS * (R - 1) >= g.M) store_form<true>(lds, row0, row_scale);
+        else store_form<false>(lds, row0, row_scale);
+    }
+
+    // EDGE: the region reaches past the last row or column; reads and writes
+    // are masked, in the same order.
+    template <bool EDGE> __device__ __forceinline__ void store_form(float *lds, int row0, float row_scale) const
+    {
+        constexpr int B = EDGE ? BE : BF;
         const Epi &e = g.e;
         const int cc = 4 * (lane % QR), rl = lane / QR;
         const int row = row0 + RS * rl;
+        // steps in which this lane has a row and a column
+        const int mine = !EDGE ? STEPS : col0 + cc < g.N ? (g.M - row + RSTEP - 1) / RSTEP : 0;
         float *const src = lds + rl * WT + cc;
-        if (col0 + WT > g.N || row0 + RS * (R - 1) >= g.M) {
-            // an edge: each group by itself, masked
-            if (col0 + cc >= g.N) return;
-#pragma unroll 1
-            for (int i = 0; i < STEPS; ++i) {
-                const int r = row + i * RSTEP;
-                if (r >= g.M) return;
-                const f32x4 s = *reinterpret_cast<const f32x4 *>(src + i * (STEP * WT));
-                float v[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = g.alpha * s[j];
-                epi_apply<4>(e, z, r, col0 + cc, g.N, v);
-                store_row<4>(g.C + (int64_t)r * g.ldc + col0 + cc, col0 + cc, g.N, v, 1.0f, 0.0f);
-            }
-            return;
-        }
         // (with a null base these addresses are never used)
         const float *gp = e.grad_pre + z * e.batch_grad_pre + (int64_t)row * e.ld_grad_pre + col();
         const float *res = e.residual + z * e.batch_residual + (int64_t)row * e.ld_residual + col();
         float *pre = e.pre + z * e.batch_pre + (int64_t)row * e.ld_pre + col();
         float *out = g.C + (int64_t)row * g.ldc + col();
+        auto read = [&](const float *p, int i, int64_t ld) {
+            p += i * RSTEP * ld;
+            if constexpr (EDGE) {
+                float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (i < mine) load_cols<4>(p, col(), g.N, x);
+                return f32x4{x[0], x[1], x[2], x[3]};
+            } else {
+                return (f32x4)*reinterpret_cast<const f32x4u *>(p);
+            }
+        };
+        auto write = [&](float *p, int i, int64_t ld, const f32x4 &v) {
+            p += i * RSTEP * ld;
+            if constexpr (EDGE) {
+                const float x[4] = {v[0], v[1], v[2], v[3]};
+                if (i < mine) store_row<4>(p, col(), g.N, x, 1.0f, 0.0f);
+            } else {
+                *reinterpret_cast<f32x4u *>(p) = v;
+            }
+        };
         // z of step i from its staged sum
         auto linear = [&](int i, const f32x4 &s) {
             const float sa = SCALES ? __shfl(row_scale, rl + i * STEP) : 1.0f;
@@ -336,12 +361,12 @@ template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
             if (e.residual)
 #pragma unroll
                 for (int b = 0; b < B; ++b)
-                    y[b] = *reinterpret_cast<const f32x4u *>(res + (int64_t)(i0 + b) * RSTEP * e.ld_residual);
+                    y[b] = read(res, i0 + b, e.ld_residual);
             if (e.grad_pre) {
                 // the sums to registers, grad_pre in their place
 #pragma unroll
                 for (int b = 0; b < B; ++b)
-                    v[b] = *reinterpret_cast<const f32x4u *>(gp + (int64_t)(i0 + b) * RSTEP * e.ld_grad_pre);
+                    v[b] = read(gp, i0 + b, e.ld_grad_pre);
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     f32x4 *const p = reinterpret_cast<f32x4 *>(at + b * (STEP * WT));
@@ -363,14 +388,14 @@ template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     v[b] = linear(i0 + b, *reinterpret_cast<const f32x4 *>(at + b * (STEP * WT)));
-                    if (e.pre) *reinterpret_cast<f32x4u *>(pre + (int64_t)(i0 + b) * RSTEP * e.ld_pre) = v[b];
+                    if (e.pre) write(pre, i0 + b, e.ld_pre, v[b]);
                 }
             } else {
 #pragma unroll 1
                 for (int b = 0; b < B; ++b) {
                     f32x4 *const p = reinterpret_cast<f32x4 *>(at + b * (STEP * WT));
                     f32x4 x = linear(i0 + b, *p);
-                    if (e.pre) *reinterpret_cast<f32x4u *>(pre + (int64_t)(i0 + b) * RSTEP * e.ld_pre) = x;
+                    if (e.pre) write(pre, i0 + b, e.ld_pre, x);
                     epi_map<false>(e.act, x);
                     *p = x;
                 }
@@ -381,8 +406,7 @@ template <int R, int WT, int RS, bool SCALES> struct StagedEpi {
 #pragma unroll
                 for (int b = 0; b < B; ++b) v[b] += y[b];
 #pragma unroll
-            for (int b = 0; b < B; ++b)
-                *reinterpret_cast<f32x4u *>(out + (int64_t)(i0 + b) * RSTEP * g.ldc) = v[b];
+            for (int b = 0; b < B; ++b) write(out, i0 + b, g.ldc, v[b]);
         }
     }
 };

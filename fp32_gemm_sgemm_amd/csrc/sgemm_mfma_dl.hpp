@@ -596,6 +596,10 @@ sgemm_mfma_dl_kernel(typename KernelArgs<EPI>::T g)
 #pragma unroll
             for (int j = 0; j < B_LOADS; ++j) bf[j] = OpB::full_slice_off(j, wave, lane, ldb, n_lim);
             const int kend = K / BK - (STAGES - 1);
+            // (the epilogue's scalar reads may be outstanding here: unless they are
+            // waited for now, every fragment wait of the loop covers all reads,
+            // 3% at 128 x 4096 x 4096)
+            if constexpr (EPI) __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));  // lgkmcnt(0)
             for (; kt < kend; ++kt) slice(kt, DlTag<true>());
         }
         for (; kt < nk; ++kt) slice(kt, DlTag<false>());
