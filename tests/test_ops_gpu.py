@@ -865,6 +865,37 @@ def test_another_stream():
     assert torch.equal(y, y2) and torch.equal(e, e2) and all(torch.equal(p, r) for p, r in zip(d, d2))
 
 
+def test_threads_on_their_streams():
+    """Calls of four threads, each on a stream of its own, at the same time."""
+    import threading
+    A, B, x, w = (dev(normal(*s, seed=i)) for i, s in enumerate(((70, 300), (200, 300), (515, 2051), (2051,))))
+
+    def calls():
+        y = sg.sgemm_epilogue(A, B, activation="gelu", transb=True)
+        q, scale = sg.quantize_e4m3(x)
+        d, dw = sg.rmsnorm_backward(x, x, w)
+        return [y, q.float(), scale, d, dw, *sg.sgemm_epilogue_backward(y, A, B, transb=True)]
+    want = calls()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for k in range(40):
+                got = calls()
+                stream.synchronize()
+                if not all(torch.equal(g, v) for g, v in zip(got, want)):
+                    bad.append((i, k))
+            stream.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
 def test_graph_replays():
     """Every operator captured once and replayed, with eager calls of the same
     operators between the replays."""
