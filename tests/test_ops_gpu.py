@@ -511,6 +511,25 @@ def test_rmsnorm_backward_many_rows(rows, D):
     ref.within(f64(dw), DW, tw)
 
 
+@pytest.mark.parametrize("rows,D", [(513, 4100), (600, 8192), (1030, 6001)])
+def test_rmsnorm_backward_long_rows_without_weight(rows, D):
+    """The form of many long rows without a weight gradient, to the last row,
+    with and without the residual stream's gradient."""
+    s, dy, w, ds = normal(rows, D, seed=1), normal(rows, D, seed=2), normal(D, seed=3), normal(rows, D, seed=4)
+    note(f"rmsnorm_backward {rows}x{D} without dw")
+    DX, _, tx, _ = ref.rmsnorm_grad(dy.astype(np.float64), s.astype(np.float64), w.astype(np.float64), 1e-6)
+    out, ok = guarded(rows, D)
+    dx, none = sg.rmsnorm_backward(dev(dy, 1), dev(s), dev(w), out=out, need_weight=False)
+    torch.cuda.synchronize()
+    assert none is None
+    ref.within(f64(out), DX, tx)
+    ok()
+    g = dev(ds)
+    sg.rmsnorm_backward(dev(dy), dev(s, 3), dev(w), dsum=g, out=g, need_weight=False)
+    torch.cuda.synchronize()
+    ref.within(f64(g), DX + ds, tx + ref.U * np.abs(DX + ds), "with the stream's")
+
+
 def test_rmsnorm_backward_of_no_rows():
     dx, dw = sg.rmsnorm_backward(torch.zeros(0, 40, device="cuda"), torch.zeros(0, 40, device="cuda"),
                                  torch.ones(40, device="cuda"))
