@@ -18,6 +18,7 @@
 #include "epilogue.hpp"
 #include "rowops.hpp"
 #include "gemm_e4m3.hpp"
+#include "e4m3_plan.hpp"
 #include "sgemm_mfma.hpp"
 #include "sgemm_mfma_dl.hpp"
 #include "sgemm_mfma_sk.hpp"
@@ -997,7 +998,7 @@ int sgemm_e4m3_workspace_size(int M, int N, int K, size_t *bytes)
     int cus = 0;
     const hipError_t e = device_cus(&cus);
     if (e != hipSuccess) return e;
-    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)e4m3_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
+    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)sgemm::e4m3_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
     return hipSuccess;
 }
 
