@@ -228,8 +228,10 @@ hipError_t run_cols(sgemm::ColArgs a, float *out, float *parts, hipStream_t stre
     const ColPlan p = col_plan(a.M, a.N);
     a.rows_per_chunk = p.rows_per_chunk;
     a.part = out ? (p.chunks > 1 ? parts : out) : nullptr;
-    const void *fn = p.tx == 64 ? reinterpret_cast<const void *>(&sgemm::col_kernel<KIND, 64>)
-                                : reinterpret_cast<const void *>(&sgemm::col_kernel<KIND, 16>);
+    const void *fn = reinterpret_cast<const void *>(&sgemm::col_kernel<KIND, 64>);
+    // (a norm's column pass is for rows past kRowCached values: never narrow)
+    if constexpr (KIND == sgemm::kColAct)
+        if (p.tx == 16) fn = reinterpret_cast<const void *>(&sgemm::col_kernel<KIND, 16>);
     const hipError_t e = launch1(fn, dim3((unsigned)p.wgs, (unsigned)p.chunks), 256, &a, stream);
     if (e != hipSuccess || !out || p.chunks <= 1) return e;
     return launch_col_sum(parts, p.chunks, a.N, out, stream);

@@ -278,3 +278,11 @@ def test_reference_codes_are_e4m3():
     torch = pytest.importorskip("torch")
     t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
     assert np.array_equal(t, ref.E4M3.astype(np.float32), equal_nan=True)
+
+
+def test_no_column_kernel_that_no_call_reaches(lib):
+    """The norm's column pass serves rows past 16384 values, so its narrow form
+    (16 lanes along at most 128 columns) would never run and is not compiled."""
+    names = open(sg.LIB_PATH, "rb").read()
+    forms = {(kind, tx): f"col_kernelILi{kind}ELi{tx}EE".encode() in names for kind in (0, 1) for tx in (16, 64)}
+    assert forms == {(0, 16): True, (0, 64): True, (1, 16): False, (1, 64): True}
