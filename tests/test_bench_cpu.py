@@ -15,3 +15,9 @@ def test_more_than_one_gpu_is_refused(capsys):
     assert "one GPU only" in capsys.readouterr().err
     assert bench.main(["--gpus", "1", "--steps", "0"]) == 2
 
+
+
+def test_traffic_was_measured_on_the_current_kernel_sources():
+    """The stored counters belong to the kernel code that is there, so the
+    benchmark reports them: a change to it means measuring them again."""
+    assert bench.read_traffic() is not None
