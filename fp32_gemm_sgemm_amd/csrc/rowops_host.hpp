@@ -55,15 +55,17 @@ RowForm row_form(int D)
 // The form of a norm or quantisation.  Where a compute unit gets more than two
 // rows, long ones go to workgroups of 512: four of them share a compute unit, and one's
 // arithmetic overlaps another's memory (8192 x 8192: quantize 74 to 61 us, 8-bit
-// norm with residual 182 to 166, norm 108 to 99, norm with residual 194 to 200;
-// 2048 x 5120: 16 to 13, 36 to 31, 19 to 18, 37 to 34; 600 x 8192: 9.3 to 8.3, 17.4
-// to 15.9, 10.9 to 10.3, 16.1 to 14.8; at 512 rows they tie or lose up to 6%).  Past 8192 values
-// that pays only where no residual is read too (4096 x 16384: quantize 77 to 69,
-// norm with residual 208 to 214), but as soon as a compute unit gets more than one
-// row (800 x 12000: quantize 17.0 to 13.8, 8-bit norm 23.3 to 19.0; 384 x 16384:
-// 11.2 to 9.9 and 15.1 to 13.0).  Fewer rows wait for one workgroup's latency,
-// which more threads shorten (1 x 8192, norm with residual: 5.0 to 4.5 us; 256 x
-// 16384, norm: 9.8 to 9.2).
+// norm with residual 182 to 166, norm 108 to 99; 2048 x 5120: 16 to 13, 36 to 31,
+// 19 to 18; 600 x 8192: 9.3 to 8.3, 17.4 to 15.9, 10.9 to 10.3; at 512 rows they tie
+// or lose up to 6%).  The norm with residual to float32, the one that moves 16
+// bytes a value, gains so too while its tensors stay in the last-level cache (600 x
+// 8192: 16.1 to 14.8, 2048 x 5120: 37 to 34) and loses 3% past it (8192 x 8192: 194
+// to 200): it goes with the others.  Past 8192 values workgroups of 512 pay only
+// where no residual is read too (4096 x 16384: quantize 77 to 69, norm with residual
+// 208 to 214), but as soon as a compute unit gets more than one row (800 x 12000:
+// quantize 17.0 to 13.8, 8-bit norm 23.3 to 19.0; 384 x 16384: 11.2 to 9.9 and 15.1
+// to 13.0).  Fewer rows wait for one workgroup's latency, which more threads shorten
+// (1 x 8192, norm with residual: 5.0 to 4.5 us; 256 x 16384, norm: 9.8 to 9.2).
 RowForm row_form_forward(int D, int rows, bool residual)
 {
     constexpr int kOneEach = 256, kTwoEach = 512;  // rows, on 256 compute units

@@ -135,8 +135,9 @@ int sgemm_f32_activation_grad_workspace(int M, int N, size_t *bytes);
  *   Y       rows x D; it may be X's, R's memory when S is not.
  *   eps     >= 0, finite.  A row of zeros with eps == 0 gives NaN (0 / 0).
  * D >= 1, rows >= 0, both <= INT_MAX - 1024; every ld >= D.  Squares are
- * float32 (|S| above 1.8e19 overflows), their sum across threads float64; S * w
- * is formed in float32.
+ * float32, their sum across threads float64; S * w is formed in float32.  So
+ * |S| above 1.8e19 overflows (Y is 0), and where eps is 0 a row of values below
+ * 1e-19 loses its squares' bits, one below 2e-23 all of them (Y is infinite).
  */
 int sgemm_rmsnorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr,
                       const float *w, float eps, float *S, int lds, float *Y, int ldy,
@@ -150,7 +151,8 @@ int sgemm_rmsnorm_f32(int rows, int D, const float *X, int ldx, const float *R, 
  *   scale = max(max_d |Y_d| / 448, 2^-126),   Q_d = e4m3(Y_d / scale),
  *
  * rounded to nearest, ties to even, so that Q_d * scale stands for Y_d (codes
- * are those of the unrounded scale, what is stored is rounded).  NaN
+ * are those of the unrounded scale, what is stored is rounded; the row's
+ * largest S * w is taken in float32).  NaN
  * values of Y become the NaN code and are left out of the row's maximum; a row
  * that holds an infinity has an infinite scale.  Q is rows x D bytes with row
  * stride ldq >= D.  Rows that start 16-byte aligned (ldq a multiple of 16) are
