@@ -60,6 +60,12 @@ class SgemmEpilogue(ctypes.Structure):
             (f"stride_{name}", ctypes.c_longlong))]
 
 
+class SgemmTensor(ctypes.Structure):
+    """sgemm_tensor of sgemm_layers.h."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("rows", "cols", "ldx", "ldy")]
+
+
 _libs = {}      # loaded builds by path
 _active = None  # path calls go to while library() is in effect (None: LIB_PATH)
 
@@ -119,6 +125,13 @@ def load(path=None):
         "sgemm_rmsnorm_f32_grad_workspace": [i, i, ctypes.POINTER(sz)],
         "sgemm_e4m3": [i, i, i, p, i, p, p, i, p, p, i, ctypes.POINTER(SgemmEpilogue), p, sz, p],
         "sgemm_e4m3_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "sgemm_layernorm_f32": [i, i, p, i, p, i, p, p, f, p, i, p, i, p],
+        "sgemm_layernorm_e4m3": [i, i, p, i, p, i, p, p, f, p, i, p, i, p, p],
+        "sgemm_layernorm_f32_grad": [i, i, p, i, p, i, p, f, p, i, p, i, p, p, p, sz, p],
+        "sgemm_layernorm_f32_grad_workspace": [i, i, ctypes.POINTER(sz)],
+        "sgemm_clip_f32": [i, ctypes.POINTER(SgemmTensor), f, f, p, p, sz, p],
+        "sgemm_clip_f32_workspace": [i, ctypes.POINTER(sz)],
+        "sgemm_norm_f32": [i, ctypes.POINTER(SgemmTensor), p, p, sz, p],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)

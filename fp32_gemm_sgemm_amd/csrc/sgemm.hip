@@ -11,12 +11,18 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "sgemm.h"
+#include "sgemm_layers.h"
 #include "sgemm_ops.h"
 #include "epilogue.hpp"
 #include "rowops.hpp"
+#include "layernorm.hpp"
+#include "clip.hpp"
 #include "gemm_e4m3.hpp"
 #include "e4m3_plan.hpp"
 #include "sgemm_mfma.hpp"
@@ -760,6 +766,8 @@ Call make_call(int transa, int transb, int M, int N, int K, float alpha,
 
 #include "rowops_host.hpp"
 #include "gemm_e4m3_host.hpp"
+#include "layernorm_host.hpp"
+#include "clip_host.hpp"
 
 }  // namespace
 
@@ -1000,6 +1008,57 @@ int sgemm_e4m3_workspace_size(int M, int N, int K, size_t *bytes)
     if (e != hipSuccess) return e;
     *bytes = M > 0 && N > 0 && K > 0 ? (size_t)sgemm::e4m3_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
     return hipSuccess;
+}
+
+}  // extern "C"
+
+extern "C" {
+
+int sgemm_layernorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr, const float *w,
+                        const float *b, float eps, float *S, int lds, float *Y, int ldy, hipStream_t stream)
+{
+    return run_layernorm(false, rows, D, X, ldx, R, ldr, w, b, eps, S, lds, Y, ldy, nullptr, 0, nullptr, stream);
+}
+
+int sgemm_layernorm_e4m3(int rows, int D, const float *X, int ldx, const float *R, int ldr, const float *w,
+                         const float *b, float eps, float *S, int lds, void *Q, int ldq, float *scale,
+                         hipStream_t stream)
+{
+    return run_layernorm(true, rows, D, X, ldx, R, ldr, w, b, eps, S, lds, nullptr, 0, Q, ldq, scale, stream);
+}
+
+int sgemm_layernorm_f32_grad(int rows, int D, const float *dY, int ldy, const float *S, int lds, const float *w,
+                             float eps, const float *dS, int ldds, float *dX, int lddx, float *dw, float *db,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return run_layernorm_grad(rows, D, dY, ldy, S, lds, w, eps, dS, ldds, dX, lddx, dw, db, workspace,
+                              workspace_bytes, stream);
+}
+
+int sgemm_layernorm_f32_grad_workspace(int rows, int D, size_t *bytes)
+{
+    if (!bytes || !row_sizes_ok(rows, D, 0.0f)) return hipErrorInvalidValue;
+    *bytes = rows > 0 ? layernorm_grad_bytes(rows, D) : 0;
+    return hipSuccess;
+}
+
+int sgemm_clip_f32(int count, const sgemm_tensor *tensors, float max_norm, float eps, float *norm, void *workspace,
+                   size_t workspace_bytes, hipStream_t stream)
+{
+    return run_clip(true, count, tensors, max_norm, eps, norm, workspace, workspace_bytes, stream);
+}
+
+int sgemm_clip_f32_workspace(int count, size_t *bytes)
+{
+    if (!bytes || count < 0) return hipErrorInvalidValue;
+    *bytes = clip_bytes(count);
+    return hipSuccess;
+}
+
+int sgemm_norm_f32(int count, const sgemm_tensor *tensors, float *norm, void *workspace, size_t workspace_bytes,
+                   hipStream_t stream)
+{
+    return run_clip(false, count, tensors, 0.0f, 0.0f, norm, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

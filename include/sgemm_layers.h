@@ -1,0 +1,130 @@
+/*
+ * libsgemm: what a model's layer needs next to the products and the operators
+ * of sgemm_ops.h, for AMD Instinct MI355X (gfx950).
+ *
+ *   - the layer norm with the residual's addition, its output in float32 or in
+ *     8 bits with one scale a row, and its gradient (sgemm_layernorm_f32,
+ *     sgemm_layernorm_e4m3, sgemm_layernorm_f32_grad);
+ *   - the norm of all elements of many tensors, and their scaling down to a
+ *     largest norm (sgemm_norm_f32, sgemm_clip_f32).
+ *
+ * Conventions are those of sgemm_ops.h: row-major device memory owned by the
+ * caller, asynchronous work on `stream` (a stream of the current device), no
+ * device allocation, no synchronisation, re-entrant; every entry point returns
+ * a hipError_t as int, and argument errors come back before anything is
+ * launched.  Float pointers and workspaces need 4- and 16-byte alignment.
+ * Results are reproducible bit for bit for the same arguments on the same
+ * device: nothing is added atomically.
+ *
+ * Overlap: an output must not overlap any other output, an input or the
+ * workspace, but for the exceptions each call names, where the two must be the
+ * same memory with the same row stride.  Tensors of one row stride that are
+ * different columns of one matrix (the halves of a tensor that holds a gated
+ * layer's two weights side by side) do not overlap.
+ */
+#ifndef SGEMM_LAYERS_H
+#define SGEMM_LAYERS_H
+
+#include "sgemm_ops.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * sgemm_layernorm_f32: per row of D values,
+ *
+ *   S = X + R,   Y = (S - mean(S)) / sqrt(var(S) + eps) * w + b,
+ *
+ * var the mean of the squared differences from the mean.
+ *
+ *   R       the residual, or NULL (S = X).
+ *   w, b    D values each, or NULL (ones, zeros).
+ *   S       rows x D, or NULL when the sum is not wanted; it may be X's or
+ *           R's memory (same pointer and ld).
+ *   Y       rows x D; it may be X's, R's memory when S is not.
+ *   eps     >= 0, finite.  A constant row with eps == 0 gives NaN (0 / 0).
+ * D >= 1, rows >= 0, both <= INT_MAX - 1024; every ld >= D.  The mean and the
+ * squares are summed in float64, so no square overflows.  A row that holds an
+ * infinity or NaN is NaN throughout.
+ */
+int sgemm_layernorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr,
+                        const float *w, const float *b, float eps, float *S, int lds, float *Y, int ldy,
+                        hipStream_t stream);
+
+/* sgemm_layernorm_e4m3: the same with the output in 8 bits and one float32
+ * scale a row, as sgemm_rmsnorm_e4m3 (Y / scale is float64 up to the
+ * rounding to a code). */
+int sgemm_layernorm_e4m3(int rows, int D, const float *X, int ldx, const float *R, int ldr,
+                         const float *w, const float *b, float eps, float *S, int lds,
+                         void *Q, int ldq, float *scale, hipStream_t stream);
+
+/*
+ * sgemm_layernorm_f32_grad: the gradient of Y = h * w + b, h = d * r, d = S -
+ * mean(S), r = 1 / sqrt(var(S) + eps), from dY.  With g = dY * w, per row
+ *
+ *   dX = r * (g - mean(g) - h * mean(g * h)) + dS,
+ *   dw = sum over rows of dY * h,   db = sum over rows of dY.
+ *
+ *   S       the norm's input sum (X + R); dX is the gradient of X and of R.
+ *   w       D values, or NULL (ones).
+ *   dS      the gradient that reaches S past the norm (the residual stream's),
+ *           or NULL; dX may be dS's memory (same pointer and ld).
+ *   dX      rows x D.
+ *   dw, db  D values each, or NULL.  rows == 0 gives zeros.
+ *   workspace  16-byte aligned, at least what
+ *           sgemm_layernorm_f32_grad_workspace gives; NULL with 0 bytes where
+ *           dw and db are NULL.  Too little is refused.
+ * The mean is summed in float64, everything else in float32 (rows past 16384
+ * values in float64): a |d| above 1.8e19 overflows (dX is then dS, or NaN).
+ * Other arguments as sgemm_layernorm_f32.
+ */
+int sgemm_layernorm_f32_grad(int rows, int D, const float *dY, int ldy, const float *S, int lds,
+                             const float *w, float eps, const float *dS, int ldds,
+                             float *dX, int lddx, float *dw, float *db,
+                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+int sgemm_layernorm_f32_grad_workspace(int rows, int D, size_t *bytes);
+
+/* One of many tensors: rows x cols elements, rows ldx (of x) and ldy (of y)
+ * elements apart; the strides matter when rows > 1. */
+typedef struct sgemm_tensor {
+    const float *x;
+    float *y;
+    long long rows, cols;
+    long long ldx, ldy;
+} sgemm_tensor;
+
+/*
+ * sgemm_clip_f32: over all elements of `count` tensors,
+ *
+ *   n = sqrt(sum x^2),   y = x * min(1, max_norm / (n + eps)).
+ *
+ *   tensors  a host array, read before the call returns.  rows and cols >= 0
+ *            (an empty tensor is left out, whatever its pointers); rows <=
+ *            INT_MAX - 1024, cols too where rows > 1, else <= 2^40; strides >=
+ *            cols.  y may be x's memory (same stride).  No two tensors may
+ *            share memory that one of them writes; the halves of one matrix
+ *            do not.
+ *   max_norm, eps   >= 0, finite.
+ *   norm     n, one float, or NULL.
+ *   workspace  16-byte aligned, at least sgemm_clip_f32_workspace's bytes.
+ * Squares and sums are float64, and the factor is taken from the unrounded n
+ * and rounded once.  A NaN, or an infinity, anywhere makes n so: the factor is
+ * then NaN, or 0.  Where every y is its x and the factor is 1 nothing is
+ * written.  Fewer than 96 tensors take two launches, or one if they are small; more take
+ * one for every 96 besides.
+ */
+int sgemm_clip_f32(int count, const sgemm_tensor *tensors, float max_norm, float eps, float *norm,
+                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+int sgemm_clip_f32_workspace(int count, size_t *bytes);
+
+/* sgemm_norm_f32: n alone; y and ldy are not read, and the same memory may be
+ * named twice (and counts twice).  Workspace as sgemm_clip_f32. */
+int sgemm_norm_f32(int count, const sgemm_tensor *tensors, float *norm,
+                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SGEMM_LAYERS_H */

@@ -1,0 +1,239 @@
+"""The operators of sgemm_layers.h on the host: exported as declared, and every
+refused call comes back as an error before any HIP call (there may be no GPU)."""
+import ctypes
+import os
+import re
+import subprocess
+import tempfile
+
+import numpy as np
+import pytest
+
+import fp32_gemm_sgemm_amd as sg
+import layers_ref as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "sgemm_layers.h")
+INVALID = 1
+P = 1 << 20  # made-up device addresses, a megabyte apart
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(sg.LIB_PATH):
+        from fp32_gemm_sgemm_amd import build
+        build.build()
+    return sg.load()
+
+
+def declared():
+    return sorted(set(re.findall(r"^\s*int\s+(sgemm_\w+)\s*\(", open(HEADER).read(), re.M)))
+
+
+@pytest.mark.parametrize("path", [sg.LIB_PATH, sg.POISON_LIB_PATH, sg.TIMELINE_LIB_PATH])
+def test_declared_functions_are_exported(lib, path):
+    out = subprocess.run(["nm", "-D", "--defined-only", path], capture_output=True, text=True, check=True).stdout
+    names = {line.split()[-1] for line in out.splitlines() if line.strip()}
+    assert len(declared()) >= 7 and set(declared()) <= names
+
+
+def layout(struct, name):
+    """The C layout of a structure of the header: offsets of its fields and its size."""
+    src = '#include <stdio.h>\n#include <stddef.h>\n#define __HIP_PLATFORM_AMD__ 1\n#include "sgemm_layers.h"\n' \
+        'int main(void){' + "".join(f'printf("%zu ", offsetof({name}, {f}));' for f, _ in struct._fields_) + \
+        f'printf("%zu", sizeof({name})); return 0;}}'
+    with tempfile.TemporaryDirectory() as d:
+        c = os.path.join(d, "t.c")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", f"-I{ROOT}/include", "-I/opt/rocm/include", c, "-o", os.path.join(d, "t")], check=True)
+        got = subprocess.run([os.path.join(d, "t")], capture_output=True, text=True).stdout.split()
+    return [int(v) for v in got]
+
+
+def test_tensor_structure_matches_the_header(lib):
+    want = [getattr(sg.SgemmTensor, f).offset for f, _ in sg.SgemmTensor._fields_]
+    assert layout(sg.SgemmTensor, "sgemm_tensor") == want + [ctypes.sizeof(sg.SgemmTensor)]
+
+
+# ---- layer norm ------------------------------------------------------------------------------------
+
+def row(lib, rows=4, D=8, X=P, ldx=8, R=2 * P, ldr=8, w=3 * P, b=7 * P, eps=1e-6, S=4 * P, lds=8, Y=5 * P, ldy=8):
+    return lib.sgemm_layernorm_f32(rows, D, X, ldx, R, ldr, w, b, eps, S, lds, Y, ldy, 0)
+
+
+def row8(lib, rows=4, D=8, X=P, ldx=8, R=2 * P, ldr=8, w=3 * P, b=7 * P, eps=1e-6, S=4 * P, lds=8, Q=5 * P, ldq=8,
+         scale=6 * P):
+    return lib.sgemm_layernorm_e4m3(rows, D, X, ldx, R, ldr, w, b, eps, S, lds, Q, ldq, scale, 0)
+
+
+def test_layer_norms_refused(lib):
+    for kw in (dict(rows=-1), dict(D=0), dict(D=-3), dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")),
+               dict(X=0), dict(X=P + 2), dict(ldx=7), dict(ldr=7), dict(R=2 * P + 1), dict(w=3 * P + 1),
+               dict(b=7 * P + 2), dict(lds=7), dict(ldx=2 ** 31 - 1), dict(rows=2 ** 31 - 1), dict(D=2 ** 31 - 1),
+               dict(S=P + 32), dict(S=P, ldx=9), dict(S=2 * P, ldr=9), dict(S=3 * P), dict(S=7 * P),
+               dict(S=P, ldx=16, lds=16, D=9)):
+        if kw.get("D") == 9:  # the same memory with the same stride is in place, 4 columns on it is not
+            kw = dict(S=P + 16, ldx=16, lds=16, D=9, ldr=9, ldy=9, ldq=9)
+            kw8 = {k: v for k, v in kw.items() if k != "ldy"}
+            kw = {k: v for k, v in kw.items() if k != "ldq"}
+            assert row(lib, **kw) == INVALID and row8(lib, **kw8) == INVALID
+            continue
+        assert row(lib, **kw) == INVALID, kw
+        assert row8(lib, **kw) == INVALID, kw
+    for kw in (dict(Y=0), dict(Y=5 * P + 2), dict(ldy=7), dict(Y=4 * P), dict(Y=3 * P), dict(Y=7 * P), dict(Y=P + 4),
+               dict(Y=P, ldx=9), dict(Y=P, S=P), dict(Y=2 * P, S=2 * P)):
+        assert row(lib, **kw) == INVALID, kw
+    for kw in (dict(Q=0), dict(ldq=7), dict(Q=P), dict(Q=2 * P), dict(Q=4 * P), dict(Q=6 * P), dict(Q=7 * P),
+               dict(scale=0), dict(scale=6 * P + 2), dict(scale=P), dict(scale=3 * P), dict(scale=4 * P),
+               dict(scale=7 * P)):
+        assert row8(lib, **kw) == INVALID, kw
+    assert row(lib, rows=0, X=0, Y=0) == 0
+
+
+def grad(lib, rows=4, D=8, dY=P, ldy=8, S=2 * P, lds=8, w=3 * P, eps=1e-6, dS=4 * P, ldds=8, dX=5 * P, lddx=8, dw=6 * P,
+         db=8 * P, ws=7 * P, ws_bytes=1 << 16):
+    return lib.sgemm_layernorm_f32_grad(rows, D, dY, ldy, S, lds, w, eps, dS, ldds, dX, lddx, dw, db, ws, ws_bytes, 0)
+
+
+def workspace(fn, *args):
+    n = ctypes.c_size_t()
+    assert fn(*args, ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_layer_norm_gradients_refused(lib):
+    rows = 40
+    need = workspace(lib.sgemm_layernorm_f32_grad_workspace, rows, 8)
+    assert need > 0
+    for kw in (dict(rows=-1), dict(D=0), dict(eps=-1.0), dict(dY=0), dict(S=0), dict(dX=0), dict(ldy=7), dict(lds=7),
+               dict(ldds=7), dict(lddx=7), dict(dw=6 * P + 2), dict(db=8 * P + 2), dict(w=2), dict(dX=P), dict(dX=2 * P),
+               dict(dX=3 * P), dict(dX=4 * P, ldds=9), dict(dw=P), dict(dw=5 * P), dict(dw=3 * P), dict(db=P),
+               dict(db=5 * P), dict(db=6 * P), dict(db=6 * P + 16), dict(ws=0, ws_bytes=0), dict(ws_bytes=need - 1),
+               dict(ws=7 * P + 4), dict(ws=P), dict(ws=5 * P), dict(ws=6 * P), dict(ws=8 * P)):
+        assert grad(lib, **{"rows": rows, **kw}) == INVALID, kw
+    # one of the sums alone still needs the workspace
+    assert grad(lib, rows=rows, dw=0, ws=0, ws_bytes=0) == INVALID
+    assert grad(lib, rows=rows, db=0, ws=0, ws_bytes=0) == INVALID
+    n = ctypes.c_size_t()
+    assert lib.sgemm_layernorm_f32_grad_workspace(-1, 8, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_layernorm_f32_grad_workspace(1, 0, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_layernorm_f32_grad_workspace(1, 8, None) == INVALID
+    assert workspace(lib.sgemm_layernorm_f32_grad_workspace, 0, 8) == 0
+
+
+# ---- norms over many tensors ---------------------------------------------------------------------------
+
+def tensors(*entries):
+    return (sg.SgemmTensor * max(len(entries), 1))(*[sg.SgemmTensor(*e) for e in entries])
+
+
+GOOD = (P, 2 * P, 4, 8, 8, 8)
+BAD_LISTS = {
+    "negative rows": [(P, 2 * P, -1, 8, 8, 8)],
+    "negative columns": [(P, 2 * P, 4, -8, 8, 8)],
+    "no input": [(0, 2 * P, 4, 8, 8, 8)],
+    "no output": [(P, 0, 4, 8, 8, 8)],
+    "misaligned input": [(P + 2, 2 * P, 4, 8, 8, 8)],
+    "misaligned output": [(P, 2 * P + 1, 4, 8, 8, 8)],
+    "short input rows": [(P, 2 * P, 4, 8, 7, 8)],
+    "short output rows": [(P, 2 * P, 4, 8, 8, 7)],
+    "too many rows": [(P, P, 2 ** 31, 1, 1, 1)],
+    "rows too long": [(P, P, 2, 2 ** 31, 2 ** 31, 2 ** 31)],
+    "a run too long": [(P, P, 1, 2 ** 41, 0, 0)],
+    "output half over its input": [(P, P + 16, 4, 8, 8, 8)],
+    "output on its input with another stride": [(P, P, 4, 8, 8, 9)],
+    "output over another's input": [GOOD, (3 * P, P, 4, 8, 8, 8)],
+    "output over another's output": [GOOD, (3 * P, 2 * P + 64, 4, 8, 8, 8)],
+    "a tensor twice in place": [(P, P, 4, 8, 8, 8), (P, P, 4, 8, 8, 8)],
+    "columns that meet": [(P, P, 4, 8, 16, 16), (P + 28, P + 28, 4, 8, 16, 16)],
+    "columns that wrap": [(P, P, 4, 8, 16, 16), (P + 64 * 2 - 4, P + 64 * 2 - 4, 2, 8, 16, 16)],
+    "inside the workspace": [(P, 7 * P, 4, 8, 8, 8)],
+    "input in the workspace": [(7 * P + 64, 2 * P, 4, 8, 8, 8)],
+    "over the norm": [(P, 6 * P, 4, 8, 8, 8)],
+    "input is the norm": [(6 * P, 2 * P, 1, 1, 1, 1)],
+}
+
+
+def clip(lib, entries, max_norm=1.0, eps=1e-6, norm=6 * P, ws=7 * P, ws_bytes=1 << 17, count=None):
+    return lib.sgemm_clip_f32(len(entries) if count is None else count, tensors(*entries), max_norm, eps, norm, ws,
+                              ws_bytes, 0)
+
+
+@pytest.mark.parametrize("what", BAD_LISTS)
+def test_lists_refused(lib, what):
+    assert clip(lib, BAD_LISTS[what]) == INVALID
+
+
+def test_clipping_refused(lib):
+    need = workspace(lib.sgemm_clip_f32_workspace, 1)
+    assert need > 0 and workspace(lib.sgemm_clip_f32_workspace, 1000) > need
+    nan, inf = float("nan"), float("inf")
+    for kw in (dict(max_norm=-1.0), dict(max_norm=nan), dict(max_norm=inf), dict(eps=-1.0), dict(eps=nan),
+               dict(eps=inf), dict(norm=6 * P + 2), dict(ws=0, ws_bytes=0), dict(ws=7 * P + 8), dict(ws_bytes=need - 1),
+               dict(count=-1), dict(norm=7 * P)):
+        assert clip(lib, [GOOD], **kw) == INVALID, kw
+    many = [(P + 256 * i, P + 256 * i, 4, 8, 8, 8) for i in range(100)]
+    assert clip(lib, many, ws_bytes=need) == INVALID  # the table of a long list needs room
+    norm = lambda entries, out=6 * P, ws=7 * P, n=1 << 17: lib.sgemm_norm_f32(len(entries), tensors(*entries), out, ws, n, 0)  # noqa: E731
+    for bad in (norm([GOOD], out=0), norm([GOOD], out=P), norm([GOOD], ws=P), norm([GOOD], n=need - 1),
+                norm([(0, 0, 4, 8, 8, 8)]), norm([(P, 0, 4, 8, 7, 8)])):
+        assert bad == INVALID
+    n = ctypes.c_size_t()
+    assert lib.sgemm_clip_f32_workspace(-1, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_clip_f32_workspace(1, None) == INVALID
+
+
+# ---- the binding ------------------------------------------------------------------------------------------
+
+def test_host_tensors_and_types_are_refused():
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 8)
+    for call in (lambda: sg.layernorm(x), lambda: sg.layernorm_e4m3(x), lambda: sg.layernorm_backward(x, x),
+                 lambda: sg.grad_norm([x]), lambda: sg.clip_grad_norm([x], 1.0), lambda: sg.grad_norm([]),
+                 lambda: sg.clip_grad_norm([], 1.0)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_planes():
+    """A tensor of any shape is one run if contiguous; else only rows with unit
+    column stride are taken."""
+    torch = pytest.importorskip("torch")
+    from fp32_gemm_sgemm_amd import layers
+    assert layers._plane(torch.zeros(3, 4, 5), "x") == (1, 60, 0)
+    assert layers._plane(torch.zeros(()), "x") == (1, 1, 0)
+    assert layers._plane(torch.zeros(4, 10)[:, :5], "x") == (4, 5, 10)
+    for bad in (torch.zeros(4, 10).T, torch.zeros(4, 10, 6)[:, :, :3], torch.zeros(10)[::2], torch.zeros(1, 4).expand(3, 4)):
+        with pytest.raises(ValueError):
+            layers._plane(bad, "x")
+    with pytest.raises(TypeError):
+        layers._plane(torch.zeros(4, dtype=torch.float64), "x")
+    host = torch.device("cpu")
+    a, b = torch.zeros(4, 10)[:, :5], torch.zeros(4, 5)
+    t = layers._tensor_list([a, b], [b, a], host)
+    assert [(e.rows, e.cols, e.ldx, e.ldy) for e in t] == [(4, 5, 10, 5), (4, 5, 5, 10)]
+    assert (t[0].x, t[0].y) == (a.data_ptr(), b.data_ptr())
+    with pytest.raises(ValueError, match="shapes"):
+        layers._tensor_list([a], [torch.zeros(5, 4)], host)
+
+
+# ---- the reference itself ------------------------------------------------------------------------------------
+
+def test_reference_layer_norm_gradient_is_the_derivative():
+    rng = np.random.default_rng(0)
+    s, w, b, dy = rng.standard_normal((3, 7)), rng.standard_normal(7), rng.standard_normal(7), rng.standard_normal((3, 7))
+
+    def f(s, w, b):
+        return float((ref.layernorm(s, w, b, 1e-3)[0] * dy).sum())
+    dx, dw, db, *_ = ref.layernorm_grad(dy, s, w, 1e-3)
+    h = 1e-6
+    for i in range(3):
+        for j in range(7):
+            e = np.zeros_like(s)
+            e[i, j] = h
+            assert abs((f(s + e, w, b) - f(s - e, w, b)) / (2 * h) - dx[i, j]) < 1e-7
+    for j in range(7):
+        e = np.zeros(7)
+        e[j] = h
+        assert abs((f(s, w + e, b) - f(s, w - e, b)) / (2 * h) - dw[j]) < 1e-7
+        assert abs((f(s, w, b + e) - f(s, w, b - e)) / (2 * h) - db[j]) < 1e-7
