@@ -17,12 +17,13 @@ from .binding import (  # noqa: F401
     sgemm_f32_strided_batched, sgemm_f32_variant, sgemm_f32_variant_ops, sgemm_f32_version,
     sgemm_f32_workspace_size, library, LIB_PATH, POISON_LIB_PATH, TIMELINE_LIB_PATH,
     SGEMM_KERNEL_MFMA, SGEMM_KERNEL_VALU, SGEMM_OP_N, SGEMM_OP_T, SGEMM_SCRATCH_BYTES,
-    ACTIVATIONS, SgemmEpilogue, SgemmTensor,
+    ACTIVATIONS, GATED_AUTO, GATED_PRODUCTS, GATED_ROWS, GATED_TILES, SgemmEpilogue, SgemmGate, SgemmTensor,
 )
 from .ops import (  # noqa: F401
     E4M3_MAX, activation_grad, gemm_e4m3, quantize_e4m3, rmsnorm, rmsnorm_backward, rmsnorm_e4m3,
     sgemm_epilogue, sgemm_epilogue_backward,
 )
 from .layers import (  # noqa: F401
-    clip_grad_norm, grad_norm, layernorm, layernorm_backward, layernorm_e4m3,
+    clip_grad_norm, gated_grad, gemm_e4m3_gated, grad_norm, layernorm, layernorm_backward, layernorm_e4m3,
+    sgemm_gated, sgemm_gated_backward,
 )

@@ -60,6 +60,16 @@ class SgemmEpilogue(ctypes.Structure):
             (f"stride_{name}", ctypes.c_longlong))]
 
 
+class SgemmGate(ctypes.Structure):
+    """sgemm_gate of sgemm_layers.h; null pointers (None) leave a part out."""
+    _fields_ = [("activation", ctypes.c_int), ("bias_gate", ctypes.c_void_p), ("bias_up", ctypes.c_void_p)] + [
+        f for name in ("pre_gate", "pre_up") for f in ((name, ctypes.c_void_p), (f"ld_{name}", ctypes.c_int))]
+
+
+# Forms of sgemm_f32_gated (SGEMM_GATED_* in sgemm_layers.h).
+GATED_AUTO, GATED_TILES, GATED_ROWS, GATED_PRODUCTS = -1, 6, 6, 7
+
+
 class SgemmTensor(ctypes.Structure):
     """sgemm_tensor of sgemm_layers.h."""
     _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
@@ -125,6 +135,12 @@ def load(path=None):
         "sgemm_rmsnorm_f32_grad_workspace": [i, i, ctypes.POINTER(sz)],
         "sgemm_e4m3": [i, i, i, p, i, p, p, i, p, p, i, ctypes.POINTER(SgemmEpilogue), p, sz, p],
         "sgemm_e4m3_workspace_size": [i, i, i, ctypes.POINTER(sz)],
+        "sgemm_f32_gated": [i, i, i, i, p, i, p, i, p, i, p, i, ctypes.POINTER(SgemmGate), p, sz, i, p],
+        "sgemm_f32_gated_workspace": [i, i, i, i, p, i, p, i, p, i, ctypes.POINTER(sz)],
+        "sgemm_e4m3_gated": [i, i, i, p, i, p, p, i, p, p, i, p, p, i, ctypes.POINTER(SgemmGate), p, sz, p],
+        "sgemm_e4m3_gated_workspace": [i, i, i, ctypes.POINTER(sz)],
+        "sgemm_f32_gated_grad": [i, i, i, p, i, p, i, p, i, p, i, p, i, p, p, p, sz, p],
+        "sgemm_f32_gated_grad_workspace": [i, i, ctypes.POINTER(sz)],
         "sgemm_layernorm_f32": [i, i, p, i, p, i, p, p, f, p, i, p, i, p],
         "sgemm_layernorm_e4m3": [i, i, p, i, p, i, p, p, f, p, i, p, i, p, p],
         "sgemm_layernorm_f32_grad": [i, i, p, i, p, i, p, f, p, i, p, i, p, p, p, sz, p],

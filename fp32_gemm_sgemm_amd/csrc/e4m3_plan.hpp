@@ -59,11 +59,12 @@ struct E4m3Plan {
     int kernel;  // a tile, or the streaming kernel -1 - i, or kE4m3None
     int splits, k_chunk;
     long long workspace_bytes;
+    double ns;  // its cost by the model
 };
 
 inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws)
 {
-    E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0};
+    E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0, 0.0};
     double best_t = -1.0;
     for (int i = 0; i < kE4m3SkinnyCount; ++i) {
         const E4m3Skinny &s = kE4m3Skinny[i];
@@ -71,7 +72,7 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
         const double per_cu = (double)ceil_div_ll(ceil_div_ll(N, 16), cus);
         const double work = (double)K / 1024.0 * per_cu * (s.wg_ns + s.row_ns * M),
                      stream = (double)N * K / kE4m3StreamBytesPerNs;
-        best = {-1 - i, 1, K > 0 ? K : 1, 0};
+        best = {-1 - i, 1, K > 0 ? K : 1, 0, 0.0};
         best_t = s.fill_ns + (work > stream ? work : stream);
         break;
     }
@@ -94,11 +95,12 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
             if (splits > 1)
                 t += kE4m3ReduceNs + 4.0 * (splits + 1) * (double)M * (double)N / kReduceBytesPerNs;
             if (best_t < 0.0 || t < best_t) {
-                best = {i, splits, splits > 1 ? (int)per : K, bytes};
+                best = {i, splits, splits > 1 ? (int)per : K, bytes, 0.0};
                 best_t = t;
             }
         }
     }
+    best.ns = best_t;
     return best;
 }
 

@@ -33,6 +33,7 @@
 
 #include "common.hpp"
 #include "epilogue.hpp"
+#include "gate.hpp"
 #include "sgemm_mfma_dl.hpp"
 
 namespace sgemm {
@@ -46,6 +47,16 @@ typedef int i32x4u __attribute__((ext_vector_type(4), aligned(1)));
 struct E4m3Args : EpiGemmArgs {
     int64_t ld_a, ld_b;
 };
+
+// With GATED, the two products of a gated feed-forward block (gate.hpp): B is the
+// gate's operand, B_up the other one.
+struct E4m3GatedArgs : E4m3Args {
+    const unsigned char *B_up;
+    int64_t ld_b_up;
+    Gate gate;
+};
+template <bool GATED> struct E4m3KernelArgs { typedef E4m3Args T; };
+template <> struct E4m3KernelArgs<true> { typedef E4m3GatedArgs T; };
 
 // 16 codes of one row from column col on; those at or past `lim` read as zero.
 __device__ __forceinline__ i32x4 load_chunk(const unsigned char *row, int col, int lim)
@@ -105,9 +116,12 @@ template <int BM, int BN, int BKF, int WAVES_M, int WAVES_N, int STAGES, int MB>
 
 // REG: the operands' rows do not start 16-byte aligned (or are too far apart
 // for 32-bit offsets): slices go through registers, loaded at any address,
-// and are written to LDS one MFMA step later.
-template <int BM, int BN, int BKF, int WAVES_M, int WAVES_N, int STAGES, int MB, bool REG>
-__global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3Args g)
+// and are written to LDS one MFMA step later.  GATED: half of a wave's blocks
+// of B are columns of the gate, the other half the same columns of B_up, so the
+// wave holds both sums of BN / 2 columns of C; a load's rows are all of one
+// block, so which operand it reads is the same for the wave.
+template <int BM, int BN, int BKF, int WAVES_M, int WAVES_N, int STAGES, int MB, bool REG, bool GATED = false>
+__global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typename E4m3KernelArgs<GATED>::T g)
 {
     typedef E4m3Traits<BM, BN, BKF, WAVES_M, WAVES_N, STAGES, MB> T;
     typedef typename T::OpA OpA;
@@ -130,9 +144,16 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
     const unsigned char *B = reinterpret_cast<const unsigned char *>(g.B) + kb;
     g.C += w.split * g.split_c;
     const int M = g.M, N = g.N, K = min(g.K - kb, g.k_chunk);
-    const int m0 = w.tm * BM, n0 = w.tn * BN;
+    constexpr int BC = GATED ? BN / 2 : BN;  // columns of C
+    const int m0 = w.tm * BM, n0 = w.tn * BC;
     A += (int64_t)m0 * g.ld_a;
     B += (int64_t)n0 * g.ld_b;
+    const unsigned char *B2 = nullptr;  // GATED: the other operand
+    int64_t ld_b2 = 0;
+    if constexpr (GATED) {
+        ld_b2 = g.ld_b_up;
+        B2 = g.B_up + kb + (int64_t)n0 * ld_b2;
+    }
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
@@ -155,18 +176,30 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
         a_row[j] = min(a_row[j], M - 1 - m0);
         a_col[j] *= 4;
     }
+    bool b_up[B_LOADS];  // GATED: load j reads B2
 #pragma unroll
     for (int j = 0; j < B_LOADS; ++j) {
         OpB::place(j, wave, lane, b_row[j], b_col[j]);
+        b_up[j] = false;
+        if constexpr (GATED) {
+            // row NB * l + b of a wave's WTN is block b's row l
+            constexpr int H = NB / 2;
+            static_assert(NB % 2 == 0 && MB % (256 / BKF) == 0, "a load's rows are of one block");
+            const int in = b_row[j] % WTN, l = in / NB, b = in % NB;
+            b_up[j] = __builtin_amdgcn_readfirstlane(b / H) != 0;
+            b_row[j] = b_row[j] / WTN * (WTN / 2) + H * l + b % H;
+        }
         b_row[j] = min(b_row[j], N - 1 - n0);
         b_col[j] *= 4;
     }
+    auto b_base_of = [&](int j) { return GATED && b_up[j] ? B2 : B; };
+    auto b_ld_of = [&](int j) { return GATED && b_up[j] ? ld_b2 : g.ld_b; };
     uint32_t a_off[A_LOADS], b_off[B_LOADS];  // direct loads: 32-bit offsets
     if constexpr (!REG) {
 #pragma unroll
         for (int j = 0; j < A_LOADS; ++j) a_off[j] = (uint32_t)a_row[j] * (uint32_t)g.ld_a + (uint32_t)a_col[j];
 #pragma unroll
-        for (int j = 0; j < B_LOADS; ++j) b_off[j] = (uint32_t)b_row[j] * (uint32_t)g.ld_b + (uint32_t)b_col[j];
+        for (int j = 0; j < B_LOADS; ++j) b_off[j] = (uint32_t)b_row[j] * (uint32_t)b_ld_of(j) + (uint32_t)b_col[j];
     }
 
     auto poison_stage = [&](int s) {
@@ -193,7 +226,7 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
         }
 #pragma unroll
         for (int j = 0; j < B_LOADS; ++j) {
-            const unsigned char *row = B + b_row[j] * g.ld_b;
+            const unsigned char *row = b_base_of(j) + b_row[j] * b_ld_of(j);
             if constexpr (FULL) rb[j] = *reinterpret_cast<const i32x4u *>(row + k0 + b_col[j]);
             else rb[j] = load_chunk(row, k0 + b_col[j], K);
         }
@@ -225,7 +258,7 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
             }
 #pragma unroll
             for (int j = 0; j < B_LOADS; ++j) {
-                const i32x4 v = load_chunk(B + b_row[j] * g.ld_b, k0 + b_col[j], K);
+                const i32x4 v = load_chunk(b_base_of(j) + b_row[j] * b_ld_of(j), k0 + b_col[j], K);
                 *reinterpret_cast<i32x4 *>(smem + s * STAGE_FLOATS + A_FLOATS +
                                            ((j * NW + wave) * 64 + lane) * 4) = v;
                 __builtin_amdgcn_sched_barrier(0);
@@ -234,6 +267,7 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
         }
         const auto ar = make_rsrc(reinterpret_cast<const float *>(A + k0), (int64_t)kOobOffset);
         const auto br = make_rsrc(reinterpret_cast<const float *>(B + k0), (int64_t)kOobOffset);
+        const auto br2 = make_rsrc(reinterpret_cast<const float *>((GATED ? B2 : B) + k0), (int64_t)kOobOffset);
 #pragma unroll
         for (int j = 0; j < A_LOADS; ++j) {
             const int off = (int)(FULL || a_col[j] < lim ? a_off[j] : kOobOffset);
@@ -244,7 +278,8 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
         for (int j = 0; j < B_LOADS; ++j) {
             const int off = (int)(FULL || b_col[j] < lim ? b_off[j] : kOobOffset);
             float *dst = smem + s * STAGE_FLOATS + A_FLOATS + (j * NW + wave) * 64 * 4;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_void *)dst, 16, off, 0, 0, 0);
+            if (GATED && b_up[j]) __builtin_amdgcn_raw_ptr_buffer_load_lds(br2, (lds_void *)dst, 16, off, 0, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_void *)dst, 16, off, 0, 0, 0);
         }
     };
 
@@ -394,31 +429,65 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
     typedef float vec_t __attribute__((ext_vector_type(NB)));
     __syncthreads();
     float *const mine = smem + wave * SHARE;
-    const StagedEpi<MB, WTN, RM, true> epi(g, 0, lane, n0 + wn * WTN);
-    float scale[RM];
+    if constexpr (GATED) {
+        // a wave's share holds a block row of both sums: the plain form's bytes
+        constexpr int H = NB / 2, WTC = WTN / 2;
+        typedef float half_t __attribute__((ext_vector_type(H)));
+        const StagedGate<MB, WTC, RM, true> epi(g.gate, g.C, g.ldc, M, N, lane, n0 + wn * WTC);
+        float scale[RM];
 #pragma unroll
-    for (int i = 0; i < RM; ++i) scale[i] = epi.row_scale(m0 + wm * WTM + i);
+        for (int i = 0; i < RM; ++i) scale[i] = epi.row_scale(m0 + wm * WTM + i);
 #pragma unroll
-    for (int i = 0; i < RM; ++i) {
-        if constexpr (kLdsPoison) {
-            lds_poison(mine + lane * (SHARE / 64), SHARE / 64);
-            lds_poison_done();
-        }
-#pragma unroll
-        for (int r = 0; r < ACC; ++r) {
-            float *p = mine + (MB == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * h + r) * WTN + NB * lr;
-            if constexpr (NB == 1) {
-                *p = acc[i][0][r];
-            } else {
-                vec_t v;
-#pragma unroll
-                for (int j = 0; j < NB; ++j) v[j] = acc[i][j][r];
-                *reinterpret_cast<vec_t *>(p) = v;
+        for (int i = 0; i < RM; ++i) {
+            if constexpr (kLdsPoison) {
+                lds_poison(mine + lane * (SHARE / 64), SHARE / 64);
+                lds_poison_done();
             }
+#pragma unroll
+            for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                for (int r = 0; r < ACC; ++r) {
+                    float *p = mine + (h2 * MB + (MB == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * h + r)) * WTC + H * lr;
+                    if constexpr (H == 1) {
+                        *p = acc[i][h2][r];
+                    } else {
+                        half_t v;
+#pragma unroll
+                        for (int j = 0; j < H; ++j) v[j] = acc[i][h2 * H + j][r];
+                        *reinterpret_cast<half_t *>(p) = v;
+                    }
+                }
+            asm volatile("" ::: "memory");
+            epi.store(mine, m0 + wm * WTM + i, scale[i]);
+            asm volatile("" ::: "memory");
         }
-        asm volatile("" ::: "memory");
-        epi.store(mine, m0 + wm * WTM + i, scale[i]);
-        asm volatile("" ::: "memory");
+    } else {
+        const StagedEpi<MB, WTN, RM, true> epi(g, 0, lane, n0 + wn * WTN);
+        float scale[RM];
+#pragma unroll
+        for (int i = 0; i < RM; ++i) scale[i] = epi.row_scale(m0 + wm * WTM + i);
+#pragma unroll
+        for (int i = 0; i < RM; ++i) {
+            if constexpr (kLdsPoison) {
+                lds_poison(mine + lane * (SHARE / 64), SHARE / 64);
+                lds_poison_done();
+            }
+#pragma unroll
+            for (int r = 0; r < ACC; ++r) {
+                float *p = mine + (MB == 32 ? 8 * (r >> 2) + 4 * h + (r & 3) : 4 * h + r) * WTN + NB * lr;
+                if constexpr (NB == 1) {
+                    *p = acc[i][0][r];
+                } else {
+                    vec_t v;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) v[j] = acc[i][j][r];
+                    *reinterpret_cast<vec_t *>(p) = v;
+                }
+            }
+            asm volatile("" ::: "memory");
+            epi.store(mine, m0 + wm * WTM + i, scale[i]);
+            asm volatile("" ::: "memory");
+        }
     }
 }
 
@@ -435,16 +504,20 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(E4m3A
 // and two column blocks per wave (half of A's reads, half the workgroups) 20.
 // Rows of A past M and of B past N are read as the last
 // one and never stored; codes past K read as zero.
-template <int W, int RM> struct SkinnyTraits {
+// GATED: both products of a gated block, the rows of both weights streamed side
+// by side against the same codes of A.
+template <int W, int RM, bool GATED = false> struct SkinnyTraits {
     static constexpr int NT = W * 64;
     static constexpr int DEPTH = 3;
-    static constexpr int LDS_FLOATS = W * RM * 256;
+    static constexpr int HALVES = GATED ? 2 : 1;
+    static constexpr int LDS_FLOATS = W * HALVES * RM * 256;
 };
 
-template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_skinny_kernel(E4m3Args g)
+template <int W, int RM, bool GATED = false>
+__global__ void __launch_bounds__(W * 64) gemm_e4m3_skinny_kernel(typename E4m3KernelArgs<GATED>::T g)
 {
-    typedef SkinnyTraits<W, RM> T;
-    constexpr int D = T::DEPTH;
+    typedef SkinnyTraits<W, RM, GATED> T;
+    constexpr int D = T::DEPTH, NH = T::HALVES;
     __shared__ __attribute__((aligned(16))) float red[T::LDS_FLOATS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -458,22 +531,28 @@ template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_ski
     // (64 bits: the last workgroup's next column can pass 2^31)
     for (int64_t c0 = 16 * (int64_t)blockIdx.x; c0 < N; c0 += 16 * (int64_t)gridDim.x) {
         const int n0 = (int)c0;
-        const unsigned char *b = reinterpret_cast<const unsigned char *>(g.B) + min(n0 + lr, N - 1) * g.ld_b;
+        const unsigned char *b[NH];
+        b[0] = reinterpret_cast<const unsigned char *>(g.B) + min(n0 + lr, N - 1) * g.ld_b;
+        if constexpr (GATED) b[1] = g.B_up + min(n0 + lr, N - 1) * g.ld_b_up;
         const unsigned char *a[RM];
 #pragma unroll
         for (int i = 0; i < RM; ++i)
             a[i] = reinterpret_cast<const unsigned char *>(g.A) + min(16 * i + lr, M - 1) * g.ld_a;
-        f32x4 acc[RM];
+        f32x4 acc[NH][RM];
 #pragma unroll
-        for (int i = 0; i < RM; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int x = 0; x < NH; ++x)
+#pragma unroll
+            for (int i = 0; i < RM; ++i) acc[x][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         struct Frag {
-            i32x4 b[2], a[RM][2];
+            i32x4 b[NH][2], a[RM][2];
         };
         // step q of this wave, wholly inside K
         auto load = [&](int q, Frag &f) {
             const int k = 128 * (wave + W * q) + 16 * h;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) f.b[c] = *reinterpret_cast<const i32x4u *>(b + k + 64 * c);
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) f.b[x][c] = *reinterpret_cast<const i32x4u *>(b[x] + k + 64 * c);
 #pragma unroll
             for (int i = 0; i < RM; ++i)
 #pragma unroll
@@ -484,9 +563,15 @@ template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_ski
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const bf16x8 y = codes_bf16(f.b[c], half);
+                    bf16x8 y[NH];
 #pragma unroll
-                    for (int i = 0; i < RM; ++i) acc[i] = mfma_bf16<16>(codes_bf16(f.a[i][c], half), y, acc[i]);
+                    for (int x = 0; x < NH; ++x) y[x] = codes_bf16(f.b[x][c], half);
+#pragma unroll
+                    for (int i = 0; i < RM; ++i) {
+                        const bf16x8 v = codes_bf16(f.a[i][c], half);
+#pragma unroll
+                        for (int x = 0; x < NH; ++x) acc[x][i] = mfma_bf16<16>(v, y[x], acc[x][i]);
+                    }
                 }
         };
         const int nfull = K / 128;                                      // whole steps of all waves
@@ -516,7 +601,8 @@ template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_ski
             Frag f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                f.b[c] = load_chunk(b, k + 64 * c, K);
+#pragma unroll
+                for (int x = 0; x < NH; ++x) f.b[x][c] = load_chunk(b[x], k + 64 * c, K);
 #pragma unroll
                 for (int i = 0; i < RM; ++i) f.a[i][c] = load_chunk(a[i], k + 64 * c, K);
             }
@@ -524,19 +610,28 @@ template <int W, int RM> __global__ void __launch_bounds__(W * 64) gemm_e4m3_ski
         }
         // the waves' partial results, added in wave order
 #pragma unroll
-        for (int i = 0; i < RM; ++i)
+        for (int x = 0; x < NH; ++x)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) red[((wave * RM + i) * 4 + r) * 64 + lane] = acc[i][r];
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) red[(((wave * NH + x) * RM + i) * 4 + r) * 64 + lane] = acc[x][i][r];
         __syncthreads();
         for (int o = tid; o < RM * 256; o += T::NT) {
-            float v[1] = {red[o]};
+            float v[1], u[1];
+            auto total = [&](int half) {
+                float s = red[half * RM * 256 + o];
 #pragma unroll
-            for (int x = 1; x < W; ++x) v[0] += red[x * RM * 256 + o];
+                for (int x = 1; x < W; ++x) s += red[(x * NH + half) * RM * 256 + o];
+                return s;
+            };
+            v[0] = total(0);
+            if constexpr (GATED) u[0] = total(1);
             // accumulator r of lane l is D[4 (l / 16) + r][l mod 16]
             const int i = o >> 8, r = (o >> 6) & 3, l = o & 63;
             const int row = 16 * i + 4 * (l >> 4) + r, col = n0 + (l & 15);
             if (row < M && col < N) {
-                epi_apply<1>(g.e, 0, row, col, N, v);
+                if constexpr (GATED) gate_apply<1>(g.gate, row, col, N, v, u);
+                else epi_apply<1>(g.e, 0, row, col, N, v);
                 g.C[(int64_t)row * g.ldc + col] = v[0];
             }
         }

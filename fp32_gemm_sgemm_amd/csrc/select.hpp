@@ -480,8 +480,10 @@ inline bool can_split(const Problem &q, long long workspace_bytes)
 // parallelism with fewer bytes.
 // epilogue: only variants with a form that applies one.  Its cost is left
 // out: it is the same few passes over C whichever plan runs.
+// strips: false keeps every row and column in the tiles.  ns receives the time.
 inline Choice select_plan(const Variant *vs, int n, const Problem &p, int cus, bool aligned16,
-                          bool lds_ok, long long workspace_bytes, bool epilogue = false)
+                          bool lds_ok, long long workspace_bytes, bool epilogue = false, bool strips = true,
+                          double *ns = nullptr)
 {
     const int op = op_index(p);
     Choice best = {-1, 1, 0, 0};
@@ -496,7 +498,8 @@ inline Choice select_plan(const Variant *vs, int n, const Problem &p, int cus, b
             const int eff = variant_eff(v, aligned16, lds_ok, pass == 0);
             if (eff <= 0) continue;
             int sms[2], sns[2];
-            const int nsm = strip_candidates(p.M, v.bm, sms), nsn = strip_candidates(p.N, v.bn, sns);
+            int nsm = strip_candidates(p.M, v.bm, sms), nsn = strip_candidates(p.N, v.bn, sns);
+            if (!strips) nsm = nsn = 1;
             for (int a = 0; a < nsm; ++a) {
                 for (int b = 0; b < nsn; ++b) {
                     const Problem q = main_block(p, sms[a], sns[b]);
@@ -535,6 +538,7 @@ inline Choice select_plan(const Variant *vs, int n, const Problem &p, int cus, b
             }
         }
     }
+    if (ns) *ns = best_t;
     return best;
 }
 

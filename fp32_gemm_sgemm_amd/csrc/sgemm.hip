@@ -23,10 +23,13 @@
 #include "rowops.hpp"
 #include "layernorm.hpp"
 #include "clip.hpp"
+#include "gate.hpp"
+#include "gated_rows.hpp"
 #include "gemm_e4m3.hpp"
 #include "e4m3_plan.hpp"
 #include "sgemm_mfma.hpp"
 #include "sgemm_mfma_dl.hpp"
+#include "sgemm_gated.hpp"
 #include "sgemm_mfma_sk.hpp"
 #include "sgemm_valu_sk.hpp"
 #include "sgemm_reduce.hpp"
@@ -768,6 +771,7 @@ Call make_call(int transa, int transb, int M, int N, int K, float alpha,
 #include "gemm_e4m3_host.hpp"
 #include "layernorm_host.hpp"
 #include "clip_host.hpp"
+#include "gated_host.hpp"
 
 }  // namespace
 
@@ -1013,6 +1017,62 @@ int sgemm_e4m3_workspace_size(int M, int N, int K, size_t *bytes)
 }  // extern "C"
 
 extern "C" {
+
+int sgemm_f32_gated(int transb, int M, int N, int K, const float *A, int lda, const float *B_gate, int ldb_gate,
+                    const float *B_up, int ldb_up, float *C, int ldc, const sgemm_gate *gate, void *workspace,
+                    size_t workspace_bytes, int form, hipStream_t stream)
+{
+    return run_gated(transb, M, N, K, A, lda, B_gate, ldb_gate, B_up, ldb_up, C, ldc, gate, workspace,
+                     workspace_bytes, form, stream);
+}
+
+int sgemm_f32_gated_workspace(int transb, int M, int N, int K, const float *A, int lda, const float *B_gate,
+                              int ldb_gate, const float *B_up, int ldb_up, size_t *bytes)
+{
+    if (!bytes || !gated_sizes_ok(transb, M, N, K, lda, ldb_gate, ldb_up, N > 1 ? N : 1)) return hipErrorInvalidValue;
+    *bytes = 0;
+    if (M == 0 || N == 0 || K == 0) return hipSuccess;
+    int cus = 0;
+    const hipError_t e = device_cus(&cus);
+    if (e != hipSuccess) return e;
+    const GatedCall c{transb, M, N, K, lda, {ldb_gate, ldb_up}, N, A, {B_gate, B_up}, nullptr, nullptr, 0};
+    *bytes = (size_t)cached_gated_plan(c, cus, LLONG_MAX).workspace_bytes;
+    return hipSuccess;
+}
+
+int sgemm_e4m3_gated(int M, int N, int K, const void *A, int lda, const float *scale_a, const void *B_gate,
+                     int ldb_gate, const float *scale_gate, const void *B_up, int ldb_up, const float *scale_up,
+                     float *C, int ldc, const sgemm_gate *gate, void *workspace, size_t workspace_bytes,
+                     hipStream_t stream)
+{
+    return run_e4m3_gated(M, N, K, A, lda, scale_a, B_gate, ldb_gate, scale_gate, B_up, ldb_up, scale_up, C, ldc,
+                          gate, workspace, workspace_bytes, stream);
+}
+
+int sgemm_e4m3_gated_workspace(int M, int N, int K, size_t *bytes)
+{
+    if (!bytes || !e4m3_sizes_ok(M, N, K)) return hipErrorInvalidValue;
+    int cus = 0;
+    const hipError_t e = device_cus(&cus);
+    if (e != hipSuccess) return e;
+    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)e4m3_gated_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
+    return hipSuccess;
+}
+
+int sgemm_f32_gated_grad(int M, int N, int activation, const float *dY, int ldy, const float *G, int ldg,
+                         const float *U, int ldu, float *dG, int lddg, float *dU, int lddu, float *dbias_gate,
+                         float *dbias_up, void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return run_gate_grad(M, N, activation, dY, ldy, G, ldg, U, ldu, dG, lddg, dU, lddu, dbias_gate, dbias_up,
+                         workspace, workspace_bytes, stream);
+}
+
+int sgemm_f32_gated_grad_workspace(int M, int N, size_t *bytes)
+{
+    if (!bytes || M < 0 || N < 0 || M > sgemm::kMaxDim || N > sgemm::kMaxDim) return hipErrorInvalidValue;
+    *bytes = gate_grad_bytes(M, N);
+    return hipSuccess;
+}
 
 int sgemm_layernorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr, const float *w,
                         const float *b, float eps, float *S, int lds, float *Y, int ldy, hipStream_t stream)

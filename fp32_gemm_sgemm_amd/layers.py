@@ -9,9 +9,255 @@ current one, no synchronisation.
 """
 import ctypes
 
-from .binding import SgemmTensor, _check, load
-from .ops import (_MAX_DIM, _elsewhere, _empty, _empty_codes, _gpu_of, _handle, _matrix, _norm_inputs, _rows,
-                  _same_gpu, _scratch, _torch, _vector)
+from .binding import GATED_AUTO, SgemmGate, SgemmTensor, _check, load, sgemm_f32_workspace_size
+from .ops import (_MAX_DIM, _activation, _elsewhere, _empty, _empty_codes, _gpu_of, _handle, _matrix, _norm_inputs,
+                  _rows, _same_gpu, _scratch, _supplied, _torch, _vector)
+
+
+# ---- the gated feed-forward block ------------------------------------------------------------
+
+def _gate(device, M, N, activation, bias_gate, bias_up, pre_gate, pre_up):
+    """SgemmGate of tensors that match an M x N output."""
+    g = SgemmGate(activation=_activation(activation))
+    if bias_gate is not None:
+        g.bias_gate = _vector(bias_gate, N, device, "bias_gate")
+    if bias_up is not None:
+        g.bias_up = _vector(bias_up, N, device, "bias_up")
+    if pre_gate is not None:
+        g.ld_pre_gate, g.pre_gate = _matrix(pre_gate, M, N, device, "pre_gate"), pre_gate.data_ptr()
+    if pre_up is not None:
+        g.ld_pre_up, g.pre_up = _matrix(pre_up, M, N, device, "pre_up"), pre_up.data_ptr()
+    return g
+
+
+def _weights(B_gate, B_up, transb, device):
+    """(K, N, row strides) of a gated block's weights."""
+    _same_gpu(device, B_gate, "B_gate")
+    _same_gpu(device, B_up, "B_up")
+    rows, cols, ldg = _rows(B_gate, "B_gate")
+    r, c, ldu = _rows(B_up, "B_up")
+    if (r, c) != (rows, cols):
+        raise ValueError(f"B_gate and B_up must have one shape, got {(rows, cols)} and {(r, c)}")
+    return (cols, rows, ldg, ldu) if transb else (rows, cols, ldg, ldu)
+
+
+def sgemm_gated(A, B_gate, B_up, *, bias_gate=None, bias_up=None, activation="silu", pre_gate=None, pre_up=None,
+                out=None, transb=False, workspace=True, stream=None, form=GATED_AUTO):
+    """act(A @ op(B_gate) + bias_gate) * (A @ op(B_up) + bias_up): both
+    projections of a gated feed-forward block, the activation and the product in
+    one call.
+
+    A is M x K, the weights are K x N each, or N x K with `transb` (one row per
+    output); they may be the two halves of one tensor.  `activation` is a name of
+    ACTIVATIONS.  `pre_gate` and `pre_up`, if given, receive the two projections
+    with their biases, which sgemm_gated_backward() needs.  `workspace` as for
+    sgemm(), `form` a forced form (GATED_* of sgemm_layers.h).
+    """
+    torch = _torch()
+    device = _gpu_of(A, "A")
+    elsewhere = _elsewhere(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return sgemm_gated(A, B_gate, B_up, bias_gate=bias_gate, bias_up=bias_up, activation=activation,
+                               pre_gate=pre_gate, pre_up=pre_up, out=out, transb=transb, workspace=workspace,
+                               form=form)
+    M, K, lda = _rows(A, "A")
+    K2, N, ldg, ldu = _weights(B_gate, B_up, transb, device)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    tb = 1 if transb else 0
+    if out is None:
+        out, ldc = _empty((M, N), device), max(N, 1)
+    else:
+        ldc = _matrix(out, M, N, device, "out")
+    g = _gate(device, M, N, activation, bias_gate, bias_up, pre_gate, pre_up)
+    operands = (tb, M, N, K, A.data_ptr(), lda, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu)
+    ws, ws_ptr, ws_bytes = None, None, 0
+    if isinstance(workspace, torch.Tensor):
+        ws_ptr, ws_bytes = _supplied(workspace, device)
+    elif workspace:
+        nbytes = ctypes.c_size_t(0)
+        _check(load().sgemm_f32_gated_workspace(*operands, ctypes.byref(nbytes)), "sgemm_f32_gated_workspace")
+        ws_bytes = nbytes.value
+        ws, ws_ptr = _scratch(ws_bytes, device)
+    code = load().sgemm_f32_gated(*operands, out.data_ptr(), ldc, ctypes.byref(g), ws_ptr, ws_bytes, form,
+                                  _handle(device))
+    del ws
+    _check(code, "sgemm_f32_gated")
+    return out
+
+
+def gated_grad(grad, pre_gate, pre_up, activation="silu", *, out_gate=None, out_up=None, dbias_gate=None,
+               dbias_up=None, stream=None):
+    """(dG, dU, dbias_gate, dbias_up) from the gradient of act(G) * U, G and U as
+    sgemm_gated() stored them: dG = grad * U * act'(G), dU = grad * act(G) and
+    their column sums, in one pass.
+
+    `out_gate`, `out_up`: a tensor to write (any of the three inputs for in
+    place), None for a new one, or False for none.  `dbias_gate`, `dbias_up`: a
+    tensor of N values, None for a new one, or False for none.
+    """
+    device = _gpu_of(grad, "grad")
+    elsewhere = _elsewhere(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gated_grad(grad, pre_gate, pre_up, activation, out_gate=out_gate, out_up=out_up,
+                              dbias_gate=dbias_gate, dbias_up=dbias_up)
+    M, N, ldy = _rows(grad, "grad")
+    act = _activation(activation)
+    ldg, ldu = _matrix(pre_gate, M, N, device, "pre_gate"), _matrix(pre_up, M, N, device, "pre_up")
+    outs, sums = [], []
+    for name, t in (("out_gate", out_gate), ("out_up", out_up)):
+        if t is False:
+            outs.append((None, None, 0))
+        elif t is None:
+            t = _empty((M, N), device)
+            outs.append((t, t.data_ptr(), max(N, 1)))
+        else:
+            outs.append((t, t.data_ptr(), _matrix(t, M, N, device, name)))
+    for name, t in (("dbias_gate", dbias_gate), ("dbias_up", dbias_up)):
+        if t is False:
+            sums.append((None, None))
+        else:
+            t = _empty((N,), device) if t is None else t
+            sums.append((t, _vector(t, N, device, name)))
+    ws, ws_ptr, nbytes = None, None, ctypes.c_size_t(0)
+    if sums[0][0] is not None or sums[1][0] is not None:
+        _check(load().sgemm_f32_gated_grad_workspace(M, N, ctypes.byref(nbytes)), "sgemm_f32_gated_grad_workspace")
+        ws, ws_ptr = _scratch(nbytes.value, device)
+    code = load().sgemm_f32_gated_grad(
+        M, N, act, grad.data_ptr(), ldy, pre_gate.data_ptr(), ldg, pre_up.data_ptr(), ldu, outs[0][1], outs[0][2],
+        outs[1][1], outs[1][2], sums[0][1], sums[1][1], ws_ptr, nbytes.value, _handle(device))
+    del ws
+    _check(code, "sgemm_f32_gated_grad")
+    return outs[0][0], outs[1][0], sums[0][0], sums[1][0]
+
+
+def _products(batch, ta, tb, M, N, K, x, ldx, sx, y, ldy, sy, beta, out, ldo, so, workspace, device):
+    """out = op(X) op(Y) + beta * out over a batch, of checked operands' addresses."""
+    ws, ws_ptr, ws_bytes = None, None, 0
+    if isinstance(workspace, _torch().Tensor):
+        ws_ptr, ws_bytes = _supplied(workspace, device)
+    elif workspace and M and N and K:
+        ws_bytes = sgemm_f32_workspace_size(ta, tb, M, N, K, ldx, ldy, ldo, batch)
+        ws, ws_ptr = _scratch(ws_bytes, device)
+    code = load().sgemm_f32_ex(ta, tb, M, N, K, 1.0, x, ldx, sx, y, ldy, sy, beta, out, ldo, so, batch, ws_ptr,
+                               ws_bytes, _handle(device), None)
+    del ws
+    _check(code, "sgemm_f32_ex")
+
+
+def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation="silu", transb=False,
+                         need=("A", "B", "bias"), workspace=True, stream=None):
+    """Gradients of y = act(A @ op(B_gate) + bias_gate) * (A @ op(B_up) + bias_up)
+    from y's: (dA, dB_gate, dB_up, dbias_gate, dbias_up), None for those `need`
+    does not name.
+
+    `pre_gate` and `pre_up` hold what sgemm_gated() stored there.  Where the
+    weights are the two halves of one tensor (side by side, or with `transb` one
+    below the other), dB_gate and dB_up are the halves of one tensor too.
+    `workspace` as for sgemm(): one given as a tensor is used by the products,
+    one after the other.
+    """
+    device = _gpu_of(grad, "grad")
+    elsewhere = _elsewhere(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return sgemm_gated_backward(grad, A, B_gate, B_up, pre_gate=pre_gate, pre_up=pre_up,
+                                        activation=activation, transb=transb, need=need, workspace=workspace)
+    _same_gpu(device, A, "A")
+    M, K, lda = _rows(A, "A")
+    K2, N, ldg, ldu = _weights(B_gate, B_up, transb, device)
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    _matrix(grad, M, N, device, "grad")
+    tb = 1 if transb else 0
+    products = "A" in need or "B" in need
+    bias = None if "bias" in need else False
+    # one tensor of both weights: its products are single ones of twice the size
+    merged = ldg == ldu and B_up.data_ptr() - B_gate.data_ptr() == 4 * N * (ldg if transb else 1) and \
+        (transb or ldg >= 2 * N)
+    # dG and dU side by side; halves that products read one by one start 16-byte aligned
+    half = N if merged else (N + 3) & ~3
+    ld = max(2 * half + 3 & ~3, 4)
+    dz = _torch().empty_strided((M, 2 * half), (ld, 1), dtype=_torch().float32, device=device) if products else None
+    _, _, dbias_gate, dbias_up = gated_grad(
+        grad, pre_gate, pre_up, activation, out_gate=dz[:, :N] if products else False,
+        out_up=dz[:, half:half + N] if products else False, dbias_gate=bias, dbias_up=bias)
+    dA = dB_gate = dB_up = None
+    z, a = (dz.data_ptr() if products else 0), A.data_ptr()
+    if "A" in need:
+        dA = _empty((M, K), device)
+        if merged:
+            _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, B_gate.data_ptr(), ldg, 0, 0.0, dA.data_ptr(), max(K, 1), 0,
+                      workspace, device)
+        else:
+            for i, (b, ldb) in enumerate(((B_gate, ldg), (B_up, ldu))):
+                _products(1, 0, 1 - tb, M, K, N, z + 4 * half * i, ld, 0, b.data_ptr(), ldb, 0, float(i),
+                          dA.data_ptr(), max(K, 1), 0, workspace, device)
+    if "B" in need:
+        if transb:
+            dB = _empty((2, N, K), device)
+            _products(2, 1, 0, N, K, M, z, ld, half, a, lda, 0, 0.0, dB.data_ptr(), max(K, 1), N * K, workspace, device)
+            dB_gate, dB_up = dB[0], dB[1]
+        elif merged:
+            dB = _empty((K, 2 * N), device)
+            _products(1, 1, 0, K, 2 * N, M, a, lda, 0, z, ld, 0, 0.0, dB.data_ptr(), max(2 * N, 1), 0, workspace, device)
+            dB_gate, dB_up = dB[:, :N], dB[:, N:]
+        else:
+            dB = _empty((2, K, N), device)
+            _products(2, 1, 0, K, N, M, a, lda, 0, z, ld, half, 0.0, dB.data_ptr(), max(N, 1), K * N, workspace, device)
+            dB_gate, dB_up = dB[0], dB[1]
+    return dA, dB_gate, dB_up, dbias_gate, dbias_up
+
+
+def gemm_e4m3_gated(A, scale_a, B_gate, scale_gate, B_up, scale_up, *, bias_gate=None, bias_up=None,
+                    activation="silu", pre_gate=None, pre_up=None, out=None, workspace=True, stream=None):
+    """sgemm_gated() for 8-bit A (M x K) and weights (N x K, one row per output),
+    in float32: act((scale_a[:, None] * A) @ (scale_gate[:, None] * B_gate).T +
+    bias_gate) times the same of B_up.
+
+    Scales are M and N float32 factors, or None for ones.
+    """
+    torch = _torch()
+    device = _gpu_of(A, "A")
+    elsewhere = _elsewhere(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_e4m3_gated(A, scale_a, B_gate, scale_gate, B_up, scale_up, bias_gate=bias_gate,
+                                   bias_up=bias_up, activation=activation, pre_gate=pre_gate, pre_up=pre_up, out=out,
+                                   workspace=workspace)
+    codes = torch.float8_e4m3fn
+    M, K, lda = _rows(A, "A", codes)
+    _same_gpu(device, B_gate, "B_gate")
+    _same_gpu(device, B_up, "B_up")
+    N, K2, ldg = _rows(B_gate, "B_gate", codes)
+    r, c, ldu = _rows(B_up, "B_up", codes)
+    if (r, c) != (N, K2):
+        raise ValueError(f"B_gate and B_up must have one shape, got {(N, K2)} and {(r, c)}")
+    if K2 != K:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    sa = _vector(scale_a, M, device, "scale_a") if scale_a is not None else None
+    sg = _vector(scale_gate, N, device, "scale_gate") if scale_gate is not None else None
+    su = _vector(scale_up, N, device, "scale_up") if scale_up is not None else None
+    if out is None:
+        out, ldc = _empty((M, N), device), max(N, 1)
+    else:
+        ldc = _matrix(out, M, N, device, "out")
+    g = _gate(device, M, N, activation, bias_gate, bias_up, pre_gate, pre_up)
+    ws, ws_ptr, ws_bytes = None, None, 0
+    if isinstance(workspace, torch.Tensor):
+        ws_ptr, ws_bytes = _supplied(workspace, device)
+    elif workspace:
+        nbytes = ctypes.c_size_t(0)
+        _check(load().sgemm_e4m3_gated_workspace(M, N, K, ctypes.byref(nbytes)), "sgemm_e4m3_gated_workspace")
+        ws_bytes = nbytes.value
+        ws, ws_ptr = _scratch(ws_bytes, device)
+    code = load().sgemm_e4m3_gated(M, N, K, A.data_ptr(), lda, sa, B_gate.data_ptr(), ldg, sg, B_up.data_ptr(), ldu,
+                                   su, out.data_ptr(), ldc, ctypes.byref(g), ws_ptr, ws_bytes, _handle(device))
+    del ws
+    _check(code, "sgemm_e4m3_gated")
+    return out
 
 
 # ---- layer norm ----------------------------------------------------------------------------

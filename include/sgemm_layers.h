@@ -2,6 +2,10 @@
  * libsgemm: what a model's layer needs next to the products and the operators
  * of sgemm_ops.h, for AMD Instinct MI355X (gfx950).
  *
+ *   - the gated feed-forward block, both projections, the activation and the
+ *     product in one call, in float32 and for 8-bit operands, and the
+ *     elementwise part of its gradient (sgemm_f32_gated, sgemm_e4m3_gated,
+ *     sgemm_f32_gated_grad);
  *   - the layer norm with the residual's addition, its output in float32 or in
  *     8 bits with one scale a row, and its gradient (sgemm_layernorm_f32,
  *     sgemm_layernorm_e4m3, sgemm_layernorm_f32_grad);
@@ -30,6 +34,94 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/*
+ * What a gated block does to its two sums, g of the gate's product and u of
+ * the other one:
+ *
+ *   g = g + bias_gate[n],  u = u + bias_up[n]
+ *   C = act(g) * u, with g and u stored to pre_gate[m][n] and pre_up[m][n]
+ *       where those are given (the gradient needs both).
+ *
+ * activation is one of SGEMM_ACT_*; a null pointer leaves its part out.
+ */
+typedef struct sgemm_gate {
+    int activation;
+    const float *bias_gate, *bias_up; /* N values each */
+    float *pre_gate;
+    int ld_pre_gate;
+    float *pre_up;
+    int ld_pre_up;
+} sgemm_gate;
+
+/* Forms of sgemm_f32_gated: the library's choice, one of the fused tiles
+ * (0 .. SGEMM_GATED_TILES - 1), the form that streams the weights for a few rows, and two
+ * plain products into the workspace. */
+#define SGEMM_GATED_AUTO (-1)
+#define SGEMM_GATED_TILES 6
+#define SGEMM_GATED_ROWS 6
+#define SGEMM_GATED_PRODUCTS 7
+
+/*
+ * sgemm_f32_gated: C = act(A x op(B_gate) + bias_gate) * (A x op(B_up) +
+ * bias_up) in float32.
+ *
+ *   A, lda   M x K, lda >= max(1, K).
+ *   B_gate, B_up  K x N (transb 0, row strides >= max(1, N)) or N x K (transb
+ *            1, >= max(1, K)) each; the halves of one tensor or two tensors.
+ *   C, ldc   M x N, ldc >= max(1, N).
+ *   workspace  optional (16-byte aligned; NULL with 0 bytes for none): lets the
+ *            two products run with K split over workgroups where the output
+ *            has few tiles.  The library's wish for these very operands (its
+ *            choice depends on their alignment; they are not read) is
+ *            sgemm_f32_gated_workspace's.
+ *   form     SGEMM_GATED_AUTO, or a form to force; one that does not serve the
+ *            call is refused with hipErrorInvalidValue.
+ * M, N, K and every ld are at most INT_MAX - 1024.  M == 0 or N == 0 does
+ * nothing; K == 0 gives the block of two sums of nothing, without reading A or
+ * the weights.
+ */
+int sgemm_f32_gated(int transb, int M, int N, int K, const float *A, int lda,
+                    const float *B_gate, int ldb_gate, const float *B_up, int ldb_up,
+                    float *C, int ldc, const sgemm_gate *gate,
+                    void *workspace, size_t workspace_bytes, int form, hipStream_t stream);
+int sgemm_f32_gated_workspace(int transb, int M, int N, int K, const float *A, int lda,
+                              const float *B_gate, int ldb_gate, const float *B_up, int ldb_up,
+                              size_t *bytes);
+
+/*
+ * sgemm_e4m3_gated: the gated block of 8-bit (e4m3) operands, float32 sums
+ * and results: A is M x K codes, B_gate and B_up N x K codes each, with
+ * scale_a (M), scale_gate and scale_up (N factors, NULL for ones) as in
+ * sgemm_e4m3, whose other conventions hold.
+ */
+int sgemm_e4m3_gated(int M, int N, int K, const void *A, int lda, const float *scale_a,
+                     const void *B_gate, int ldb_gate, const float *scale_gate,
+                     const void *B_up, int ldb_up, const float *scale_up,
+                     float *C, int ldc, const sgemm_gate *gate,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream);
+int sgemm_e4m3_gated_workspace(int M, int N, int K, size_t *bytes);
+
+/*
+ * sgemm_f32_gated_grad: the elementwise part of a gated block's gradient in
+ * one pass, from its output's gradient and the stored g and u,
+ *
+ *   dG = dY * U * act'(G),   dU = dY * act(G),
+ *   dbias_gate, dbias_up = the column sums of dG and of dU.
+ *
+ *   dG, dU   M x N each, or NULL; each may be the memory of one of the inputs
+ *            (same pointer and ld).
+ *   dbias_gate, dbias_up   N values each, or NULL.  M == 0 gives zeros.
+ *   workspace  16-byte aligned, at least sgemm_f32_gated_grad_workspace's
+ *            bytes; NULL with 0 bytes where both sums are NULL.  Too little is
+ *            refused.
+ * M, N <= INT_MAX - 1024, ld >= max(1, N).  N == 0 does nothing.
+ */
+int sgemm_f32_gated_grad(int M, int N, int activation, const float *dY, int ldy,
+                         const float *G, int ldg, const float *U, int ldu,
+                         float *dG, int lddg, float *dU, int lddu, float *dbias_gate, float *dbias_up,
+                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+int sgemm_f32_gated_grad_workspace(int M, int N, size_t *bytes);
 
 /*
  * sgemm_layernorm_f32: per row of D values,

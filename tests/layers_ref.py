@@ -66,4 +66,42 @@ def clip(tensors, max_norm, eps):
     return n, min(1.0, f) if not np.isnan(f) else f
 
 
-__all__ = ["ref", "U", "VAR_ERR", "layernorm", "layernorm_grad", "clip"]
+# ---- the gated block ------------------------------------------------------------------------------
+
+def gated(A, Bg, Bu, K, bias_gate=None, bias_up=None, activation="silu"):
+    """(Y, G, U, bounds of each) of float64 operands (K x N weights): the two
+    products' bounds of ops_ref.product, the activation's, and the product of
+    the two values."""
+    G, _, tg, _ = ref.product(A, Bg, K, 1.0, bias_gate)
+    U_, _, tu, _ = ref.product(A, Bu, K, 1.0, bias_up)
+    a = ref.act(G, activation)
+    ta = ref.LIPSCHITZ * tg + (ref.ACT_ERR * np.abs(G) if activation != "none" else 0)
+    Y = a * U_
+    return Y, G, U_, np.abs(U_) * ta + (np.abs(a) + ta) * tu + 2 * U * np.abs(Y) + 1e-37, tg, tu
+
+
+def gated_grad(dy, G, U_, activation):
+    """(dG, dU, their column sums, bounds of the four)."""
+    s, a = ref.slope(G, activation), ref.act(G, activation)
+    dg, du = dy * U_ * s, dy * a
+    none = activation == "none"
+    tg = np.abs(dy * U_) * (0 if none else ref.SLOPE_ERR) + 2 * U * np.abs(dg) + 1e-37
+    tu = np.abs(dy) * np.abs(G) * (0 if none else ref.ACT_ERR) + U * np.abs(du) + 1e-37
+    n = (dy.shape[0] + 1) * U
+    return (dg, du, dg.sum(0), du.sum(0), tg, tu, tg.sum(0) + n * np.abs(dg).sum(0) + 1e-37,
+            tu.sum(0) + n * np.abs(du).sum(0) + 1e-37)
+
+
+def gated_backward(dy, A, Bg, Bu, G, U_, activation):
+    """(dA, dBg, dBu, bounds of each) of float64 operands (K x N weights)."""
+    dg, du, _, _, tg, tu, _, _ = gated_grad(dy, G, U_, activation)
+    M, N = dy.shape
+
+    def prod(x, y, n, tx):
+        """x @ y, x off by tx, sums of n float32 terms."""
+        return x @ y, (n + 3) * U * (np.abs(x) @ np.abs(y)) + tx @ np.abs(y)
+    a, ta = prod(dg, Bg.T, 2 * N, tg)
+    b, tb = prod(du, Bu.T, 2 * N, tu)
+    dA = a + b
+    (x, tx), (y, ty) = prod(dg.T, A, M, tg.T), prod(du.T, A, M, tu.T)
+    return dA, x.T, y.T, ta + tb + U * np.abs(dA) + 1e-37, tx.T + 1e-37, ty.T + 1e-37

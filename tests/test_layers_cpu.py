@@ -34,7 +34,7 @@ def declared():
 def test_declared_functions_are_exported(lib, path):
     out = subprocess.run(["nm", "-D", "--defined-only", path], capture_output=True, text=True, check=True).stdout
     names = {line.split()[-1] for line in out.splitlines() if line.strip()}
-    assert len(declared()) >= 7 and set(declared()) <= names
+    assert len(declared()) == 13 and set(declared()) <= names
 
 
 def layout(struct, name):
@@ -53,6 +53,124 @@ def layout(struct, name):
 def test_tensor_structure_matches_the_header(lib):
     want = [getattr(sg.SgemmTensor, f).offset for f, _ in sg.SgemmTensor._fields_]
     assert layout(sg.SgemmTensor, "sgemm_tensor") == want + [ctypes.sizeof(sg.SgemmTensor)]
+
+
+def test_gate_structure_matches_the_header(lib):
+    want = [getattr(sg.SgemmGate, f).offset for f, _ in sg.SgemmGate._fields_]
+    assert layout(sg.SgemmGate, "sgemm_gate") == want + [ctypes.sizeof(sg.SgemmGate)]
+
+
+def test_forms_match_the_header():
+    text = open(HEADER).read()
+    for name in ("TILES", "ROWS", "PRODUCTS"):
+        assert re.search(rf"#define\s+SGEMM_GATED_{name}\s+{getattr(sg, 'GATED_' + name)}\b", text)
+    assert sg.GATED_AUTO == -1
+
+
+# ---- the gated block ---------------------------------------------------------------------------------
+
+def gate(**kw):
+    e = sg.SgemmGate()
+    for k, v in kw.items():
+        setattr(e, k, v)
+    return e
+
+
+def gated(lib, e=None, tb=0, M=8, N=8, K=8, A=P, lda=8, Bg=2 * P, ldg=8, Bu=3 * P, ldu=8, C=4 * P, ldc=8, ws=0, ws_bytes=0,
+          form=-1):
+    e = gate() if e is None else e
+    return lib.sgemm_f32_gated(tb, M, N, K, A, lda, Bg, ldg, Bu, ldu, C, ldc, ctypes.byref(e), ws, ws_bytes, form, 0)
+
+
+def gated8(lib, e=None, M=8, N=8, K=8, A=P, lda=8, sa=8 * P, Bg=2 * P, ldg=8, sgate=9 * P, Bu=3 * P, ldu=8, su=10 * P, C=4 * P,
+           ldc=8, ws=0, ws_bytes=0):
+    e = gate() if e is None else e
+    return lib.sgemm_e4m3_gated(M, N, K, A, lda, sa, Bg, ldg, sgate, Bu, ldu, su, C, ldc, ctypes.byref(e), ws, ws_bytes, 0)
+
+
+BAD_GATES = {
+    "unknown activation": dict(activation=5),
+    "negative activation": dict(activation=-1),
+    "misaligned gate bias": dict(bias_gate=5 * P + 2),
+    "misaligned up bias": dict(bias_up=5 * P + 1),
+    "bias over C": dict(bias_gate=4 * P + 4),
+    "up bias over C": dict(bias_up=4 * P),
+    "short pre_gate rows": dict(pre_gate=5 * P, ld_pre_gate=7),
+    "short pre_up rows": dict(pre_up=5 * P, ld_pre_up=7),
+    "misaligned pre_gate": dict(pre_gate=5 * P + 2, ld_pre_gate=8),
+    "pre_gate over C": dict(pre_gate=4 * P, ld_pre_gate=8),
+    "pre_gate over A": dict(pre_gate=P, ld_pre_gate=8),
+    "pre_gate over the gate's weights": dict(pre_gate=2 * P, ld_pre_gate=8),
+    "pre_up over the other weights": dict(pre_up=3 * P, ld_pre_up=8),
+    "pre_up over pre_gate": dict(pre_up=5 * P, ld_pre_up=8, pre_gate=5 * P, ld_pre_gate=8),
+    "pre_up over the last of pre_gate": dict(pre_up=5 * P + 252, ld_pre_up=9, pre_gate=5 * P, ld_pre_gate=8),
+    "pre_gate over its bias": dict(pre_gate=5 * P, ld_pre_gate=8, bias_gate=5 * P),
+    "pre_up over the gate's bias": dict(pre_up=5 * P, ld_pre_up=8, bias_gate=5 * P),
+    "columns that meet": dict(pre_gate=5 * P, ld_pre_gate=16, pre_up=5 * P + 28, ld_pre_up=16),
+    "huge rows": dict(pre_gate=5 * P, ld_pre_gate=2 ** 31 - 1),
+}
+
+
+@pytest.mark.parametrize("what", BAD_GATES)
+def test_gates_refused(lib, what):
+    assert gated(lib, gate(**BAD_GATES[what])) == INVALID
+    assert gated8(lib, gate(**BAD_GATES[what])) == INVALID
+
+
+def test_gated_blocks_refused(lib):
+    for kw in (dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=7), dict(ldg=7), dict(ldu=7), dict(ldc=7), dict(A=0), dict(Bg=0),
+               dict(Bu=0), dict(C=0), dict(C=4 * P + 2), dict(C=P), dict(C=2 * P), dict(C=3 * P + 16),
+               dict(ws=4 * P, ws_bytes=64), dict(ws=P, ws_bytes=64), dict(ws=2 * P, ws_bytes=64),
+               dict(ws=3 * P, ws_bytes=64), dict(ws=6 * P + 4, ws_bytes=64), dict(M=2 ** 31 - 1), dict(K=2 ** 31 - 1),
+               dict(lda=2 ** 31 - 1)):
+        assert gated(lib, **kw) == INVALID, kw
+        assert gated8(lib, **kw) == INVALID, kw
+    for kw in (dict(tb=2), dict(tb=-1), dict(A=P + 2), dict(Bg=2 * P + 1), dict(Bu=3 * P + 2), dict(form=-2), dict(form=8),
+               dict(form=sg.GATED_PRODUCTS), dict(form=sg.GATED_PRODUCTS, ws=6 * P, ws_bytes=2 * 8 * 8 * 4 - 16),
+               # a tile whose offsets would not fit in 32 bits
+               dict(form=0, lda=1 << 23), dict(form=2, tb=1, ldg=1 << 23), dict(form=1, ldu=1 << 26)):
+        assert gated(lib, **kw) == INVALID, kw
+    for kw in (dict(sa=8 * P + 2), dict(sgate=9 * P + 1), dict(su=10 * P + 2), dict(C=8 * P), dict(C=9 * P), dict(C=10 * P),
+               dict(ws=8 * P, ws_bytes=64), dict(ws=10 * P, ws_bytes=64)):
+        assert gated8(lib, **kw) == INVALID, kw
+    assert lib.sgemm_f32_gated(0, 8, 8, 8, P, 8, 2 * P, 8, 3 * P, 8, 4 * P, 8, None, 0, 0, -1, 0) == INVALID
+    assert lib.sgemm_e4m3_gated(8, 8, 8, P, 8, None, 2 * P, 8, None, 3 * P, 8, None, 4 * P, 8, None, 0, 0, 0) == INVALID
+    # the workspace must keep clear of what the gate reads and stores
+    for e in (gate(bias_up=6 * P), gate(pre_up=6 * P, ld_pre_up=8)):
+        assert gated(lib, e, ws=6 * P, ws_bytes=64) == INVALID
+        assert gated8(lib, e, ws=6 * P, ws_bytes=64) == INVALID
+    # nothing to do is no error, whatever the pointers
+    assert gated(lib, M=0, A=0, Bg=0, Bu=0, C=0) == 0
+    assert gated8(lib, N=0, A=0, Bg=0, Bu=0, C=0) == 0
+    n = ctypes.c_size_t()
+    assert lib.sgemm_f32_gated_workspace(0, -1, 8, 8, P, 8, P, 8, P, 8, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_f32_gated_workspace(0, 8, 8, 8, P, 8, P, 8, P, 8, None) == INVALID
+    assert lib.sgemm_f32_gated_workspace(1, 8, 8, 8, P, 8, P, 8, P, 7, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_e4m3_gated_workspace(1, 1, -1, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_e4m3_gated_workspace(1, 1, 1, None) == INVALID
+
+
+def gate_grad(lib, M=40, N=8, act=4, dY=P, ldy=8, G=2 * P, ldg=8, U=3 * P, ldu=8, dG=4 * P, lddg=8, dU=5 * P, lddu=8, bg=6 * P,
+              bu=8 * P, ws=7 * P, ws_bytes=1 << 18):
+    return lib.sgemm_f32_gated_grad(M, N, act, dY, ldy, G, ldg, U, ldu, dG, lddg, dU, lddu, bg, bu, ws, ws_bytes, 0)
+
+
+def test_gate_gradients_refused(lib):
+    M = 4000
+    need = workspace(lib.sgemm_f32_gated_grad_workspace, M, 8)
+    assert need > 0
+    for kw in (dict(M=-1), dict(N=-1), dict(act=5), dict(act=-1), dict(dY=0), dict(G=0), dict(U=0), dict(ldy=7), dict(ldg=7),
+               dict(ldu=7), dict(lddg=7), dict(lddu=7), dict(dG=4 * P + 2), dict(dU=5 * P + 2), dict(bg=6 * P + 2),
+               dict(bu=8 * P + 1), dict(dG=P, lddg=9), dict(dG=P + 32), dict(dU=2 * P + 32), dict(dU=3 * P, lddu=9),
+               dict(dG=5 * P), dict(dG=P, dU=P), dict(bg=P), dict(bg=4 * P), dict(bu=5 * P), dict(bu=6 * P), dict(bu=2 * P),
+               dict(ws=0, ws_bytes=0), dict(ws_bytes=need - 1), dict(ws=7 * P + 8), dict(ws=P), dict(ws=3 * P), dict(ws=4 * P),
+               dict(ws=5 * P), dict(ws=6 * P), dict(ws=8 * P)):
+        assert gate_grad(lib, **{"M": M, **kw}) == INVALID, kw
+    assert gate_grad(lib, N=0, dY=0) == 0
+    assert gate_grad(lib, dG=None, dU=None, bg=None, bu=None, ws=0, ws_bytes=0) == 0  # nothing asked for
+    n = ctypes.c_size_t()
+    assert lib.sgemm_f32_gated_grad_workspace(-1, 8, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_f32_gated_grad_workspace(8, 8, None) == INVALID
 
 
 # ---- layer norm ------------------------------------------------------------------------------------
@@ -187,9 +305,11 @@ def test_clipping_refused(lib):
 
 def test_host_tensors_and_types_are_refused():
     torch = pytest.importorskip("torch")
-    x = torch.zeros(4, 8)
+    x, q = torch.zeros(4, 8), torch.zeros(4, 8, dtype=torch.uint8).view(torch.float8_e4m3fn)
     for call in (lambda: sg.layernorm(x), lambda: sg.layernorm_e4m3(x), lambda: sg.layernorm_backward(x, x),
-                 lambda: sg.grad_norm([x]), lambda: sg.clip_grad_norm([x], 1.0), lambda: sg.grad_norm([]),
+                 lambda: sg.sgemm_gated(x, x, x), lambda: sg.gated_grad(x, x, x),
+                 lambda: sg.sgemm_gated_backward(x, x, x, x, pre_gate=x, pre_up=x),
+                 lambda: sg.gemm_e4m3_gated(q, None, q, None, q, None), lambda: sg.grad_norm([x]), lambda: sg.clip_grad_norm([x], 1.0), lambda: sg.grad_norm([]),
                  lambda: sg.clip_grad_norm([], 1.0)):
         with pytest.raises(ValueError):
             call()
@@ -237,3 +357,24 @@ def test_reference_layer_norm_gradient_is_the_derivative():
         e[j] = h
         assert abs((f(s, w + e, b) - f(s, w - e, b)) / (2 * h) - dw[j]) < 1e-7
         assert abs((f(s, w, b + e) - f(s, w, b - e)) / (2 * h) - db[j]) < 1e-7
+
+
+def test_reference_gated_gradient_is_the_derivative():
+    rng = np.random.default_rng(1)
+    A, Bg, Bu, dy = (rng.standard_normal(s) for s in ((3, 4), (4, 5), (4, 5), (3, 5)))
+    bg, bu = rng.standard_normal(5), rng.standard_normal(5)
+    for name in ref.ref.ACTS:
+        def f(A, Bg, Bu, bg, bu):
+            return float((ref.gated(A, Bg, Bu, 4, bg, bu, name)[0] * dy).sum())
+        _, G, U, *_ = ref.gated(A, Bg, Bu, 4, bg, bu, name)
+        _, _, dbg, dbu, *_ = ref.gated_grad(dy, G, U, name)
+        dA, dBg, dBu, *_ = ref.gated_backward(dy, A, Bg, Bu, G, U, name)
+        h = 1e-6
+        for k, want in enumerate((dA, dBg, dBu, dbg, dbu)):
+            for i in np.ndindex(want.shape):
+                args = [A, Bg, Bu, bg, bu]
+                e = np.zeros_like(args[k])
+                e[i] = h
+                up, down = list(args), list(args)
+                up[k], down[k] = args[k] + e, args[k] - e
+                assert abs((f(*up) - f(*down)) / (2 * h) - want[i]) < 1e-6, (name, k, i)
