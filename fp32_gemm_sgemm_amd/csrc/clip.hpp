@@ -8,15 +8,18 @@
 // cannot overflow, at no cost: the kernels are bound by memory (two conversions
 // and sums an element against 4 bytes read).
 //
-// The tensors' elements are cut into chunks of kClipChunk; a workgroup takes a
-// run of consecutive chunks, so it looks its first tensor up once and walks the
-// table from there.  clip_norm_kernel leaves one partial sum a workgroup.
+// The tensors' elements are cut into chunks of kClipChunk, dealt to the
+// workgroups in turns.  clip_norm_kernel leaves one partial sum a workgroup.
 // clip_scale_kernel's workgroups each add those partial sums again, in the same
 // order and so to the same bits, instead of waiting for a kernel that would do
 // it for all: 2048 numbers from L2 cost about 2 us against 3 for a launch.  It
-// takes the same run of chunks from its end, where the last level cache still
-// holds what the norm's pass read last.  Where there is little to do one
-// workgroup does all of it in one launch.
+// takes the turns from the last one back, whose values the last level cache
+// still holds from the norm's pass, and passes that cache by with its own loads
+// and stores, which are the last use of a value in this call.  Measured on 2^29
+// values (2 GiB) as bare loops, microseconds for both kernels: 1056 so, 1171 with
+// plain loads and stores, 1128 where a workgroup takes consecutive chunks; on 2^24
+// values 29.0, 32.2 and 32.6.  Where there is little to do one workgroup does all of it in
+// one launch.
 #pragma once
 
 #include "common.hpp"
@@ -44,7 +47,7 @@ struct ClipArgs {
     double *part;             // one sum a workgroup
     float *norm;
     double max_norm, eps;
-    int count, chunks, per_wg, parts;
+    int count, chunks, parts;
     int in_place;             // every y is its x: nothing to write where c is 1
     ClipTensor here[kClipInline];
 };
@@ -58,9 +61,12 @@ __host__ __device__ inline int clip_rows(int64_t cols)
 }
 __host__ __device__ inline int64_t clip_row_chunks(int64_t cols) { return (cols + kClipChunk - 1) / kClipChunk; }
 
-// Calls f(element offset in x, offset in y, columns from there on to the row's end) for
-// each group of four of chunk k of tensor e, dealt to NT threads.
-template <int NT, typename F> __device__ __forceinline__ void clip_chunk(const ClipTensor &e, int k, F f)
+// Chunk k of tensor e, dealt to NT threads in groups of four: whole(offset in x,
+// offset in y) once where the chunk is kClipChunk elements of one row (a thread's
+// groups are then 4 NT apart), else part(offsets, columns from there on to the row's end)
+// for each group.
+template <int NT, typename W, typename P>
+__device__ __forceinline__ void clip_chunk(const ClipTensor &e, int k, W whole, P part)
 {
     const int tid = threadIdx.x;
     const int rpc = clip_rows(e.cols);
@@ -71,13 +77,12 @@ template <int NT, typename F> __device__ __forceinline__ void clip_chunk(const C
             row = k / per_row;
             col = (k - row * per_row) * kClipChunk;
         }
-        const int n = (int)(e.cols - col < kClipChunk ? e.cols - col : kClipChunk);
-        const int64_t ix = row * e.ldx + col, iy = row * e.ldy + col;
-#pragma unroll
-        for (int j = 0; j < kClipChunk / (4 * NT); ++j) {
-            const int i = 4 * (j * NT + tid);
-            if (i < n) f(ix + i, iy + i, n - i);
+        const int64_t ix = row * e.ldx + col, iy = row * e.ldy + col, left = e.cols - col;
+        if (left >= kClipChunk) {
+            whole(ix + 4 * tid, iy + 4 * tid);
+            return;
         }
+        for (int i = 4 * tid; i < (int)left; i += 4 * NT) part(ix + i, iy + i, (int)left - i);
     } else {
         const int64_t row0 = (int64_t)k * rpc;
         const int rows = (int)(e.rows - row0 < rpc ? e.rows - row0 : rpc);
@@ -85,15 +90,15 @@ template <int NT, typename F> __device__ __forceinline__ void clip_chunk(const C
         const int all = rows * (int)groups;
         for (int i = tid; i < all; i += NT) {
             const unsigned r = (unsigned)i / groups, c = 4 * ((unsigned)i - r * groups);
-            f((row0 + r) * e.ldx + c, (row0 + r) * e.ldy + c, (int)(cols - c));
+            part((row0 + r) * e.ldx + c, (row0 + r) * e.ldy + c, (int)(cols - c));
         }
     }
 }
 
-// The tensor that chunk c belongs to: the last one whose first chunk is not past it.
-__device__ __forceinline__ int clip_find(const ClipTensor *table, int count, int c)
+// The tensor that chunk c belongs to, among lo .. hi: the last one whose first chunk is
+// not past it.
+__device__ __forceinline__ int clip_find(const ClipTensor *table, int lo, int hi, int c)
 {
-    int lo = 0, hi = count - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (table[mid].first <= c) lo = mid;
@@ -102,40 +107,95 @@ __device__ __forceinline__ int clip_find(const ClipTensor *table, int count, int
     return lo;
 }
 
-// This thread's sum of squares over chunks [c0, c1).
+// Walks the table along with a workgroup's chunks, forwards or back.
+struct ClipWalk {
+    const ClipTensor *const table;
+    const int count, chunks;
+    ClipTensor e;     // the present tensor
+    int i, end;       // its place, and the first chunk past it
+
+    __device__ __forceinline__ ClipWalk(const ClipTensor *t, int n, int all) : table(t), count(n), chunks(all), i(0), end(0) {}
+
+    __device__ __forceinline__ void to(int at)
+    {
+        i = at;
+        e = table[i];
+        end = i + 1 < count ? table[i + 1].first : chunks;
+    }
+    __device__ __forceinline__ void start(int c) { to(clip_find(table, 0, count - 1, c)); }
+    __device__ __forceinline__ void forwards(int c)
+    {
+        if (c < end) return;
+        to(i + 1);
+        if (c >= end) to(clip_find(table, i + 1, count - 1, c));
+    }
+    __device__ __forceinline__ void back(int c)
+    {
+        if (c >= e.first) return;
+        to(i - 1);
+        if (c < e.first) to(clip_find(table, 0, i - 1, c));
+    }
+};
+
+// This thread's sum of squares over chunks first, first + step, ...
 template <int NT>
-__device__ __forceinline__ double clip_squares(const ClipArgs &a, const ClipTensor *table, int c0, int c1)
+__device__ __forceinline__ double clip_squares(const ClipArgs &a, const ClipTensor *table, int first, int step)
 {
     double sum = 0.0;
-    if (c0 >= c1) return sum;
-    int i = clip_find(table, a.count, c0);
-    for (int c = c0; c < c1; ++c) {
-        while (i + 1 < a.count && table[i + 1].first <= c) ++i;
-        const ClipTensor e = table[i];
-        clip_chunk<NT>(e, c - e.first, [&](int64_t ix, int64_t, int left) {
-            float v[4];
-            load_cols<4>(e.x + ix, 0, left, v);
+    if (first >= a.chunks) return sum;
+    constexpr int G = kClipChunk / (4 * NT);  // groups of a thread
+    ClipWalk w(table, a.count, a.chunks);
+    w.start(first);
+    for (int64_t c = first; c < a.chunks; c += step) {
+        w.forwards((int)c);
+        clip_chunk<NT>(
+            w.e, (int)c - w.e.first,
+            [&](int64_t ix, int64_t) {
+                f32x4 v[G];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum += (double)v[j] * (double)v[j];
-        });
+                for (int j = 0; j < G; ++j) v[j] = *reinterpret_cast<const f32x4u *>(w.e.x + ix + j * 4 * NT);
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sum += (double)v[j][q] * (double)v[j][q];
+            },
+            [&](int64_t ix, int64_t, int left) {
+                float v[4];
+                load_cols<4>(w.e.x + ix, 0, left, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sum += (double)v[q] * (double)v[q];
+            });
     }
     return sum;
 }
 
-// y = c x over chunks [c0, c1), from the last one back.
+// y = c x over the same chunks, from the last one back.
 template <int NT>
-__device__ __forceinline__ void clip_write(const ClipArgs &a, const ClipTensor *table, int c0, int c1, float c)
+__device__ __forceinline__ void clip_write(const ClipArgs &a, const ClipTensor *table, int first, int step, float c)
 {
-    if (c0 >= c1 || (a.in_place && c == 1.0f)) return;
-    int i = clip_find(table, a.count, c1 - 1);
-    for (int k = c1 - 1; k >= c0; --k) {
-        while (table[i].first > k) --i;
-        const ClipTensor e = table[i];
-        clip_chunk<NT>(e, k - e.first, [&](int64_t ix, int64_t iy, int left) {
-            float v[4];
-            load_cols<4>(e.x + ix, 0, left, v);
-            store_row<4>(e.y + iy, 0, left, v, c, 0.0f);
-        });
+    if (first >= a.chunks || (a.in_place && c == 1.0f)) return;
+    constexpr int G = kClipChunk / (4 * NT);
+    ClipWalk w(table, a.count, a.chunks);
+    int64_t k = first + (int64_t)((a.chunks - 1 - first) / step) * step;
+    w.start((int)k);
+    for (; k >= first; k -= step) {
+        w.back((int)k);
+        clip_chunk<NT>(
+            w.e, (int)k - w.e.first,
+            [&](int64_t ix, int64_t iy) {
+                f32x4u v[G];
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    v[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4u *>(w.e.x + ix + j * 4 * NT));
+#pragma unroll
+                for (int j = 0; j < G; ++j)
+                    __builtin_nontemporal_store(v[j] * c, reinterpret_cast<f32x4u *>(w.e.y + iy + j * 4 * NT));
+            },
+            [&](int64_t ix, int64_t iy, int left) {
+                float v[4];
+                load_cols<4>(w.e.x + ix, 0, left, v);
+                store_row<4>(w.e.y + iy, 0, left, v, c, 0.0f);
+            });
     }
 }
 
@@ -150,10 +210,7 @@ __device__ __forceinline__ float clip_factor(const ClipArgs &a, double total)
 template <bool HERE> __global__ void __launch_bounds__(kClipThreads) clip_norm_kernel(ClipArgs a)
 {
     __shared__ RowSums<kClipThreads> sums;
-    const ClipTensor *const table = HERE ? a.here : a.table;
-    const int64_t c0 = (int64_t)blockIdx.x * a.per_wg;
-    const int c1 = (int)(c0 + a.per_wg < a.chunks ? c0 + a.per_wg : a.chunks);
-    double sum[1] = {clip_squares<kClipThreads>(a, table, (int)c0, c1)};
+    double sum[1] = {clip_squares<kClipThreads>(a, HERE ? a.here : a.table, (int)blockIdx.x, (int)gridDim.x)};
     int turn = 0;
     row_all<kClipThreads, AddOp>(sum, &sums, turn);
     if (threadIdx.x == 0) a.part[blockIdx.x] = sum[0];
@@ -168,12 +225,9 @@ template <bool HERE, bool WRITE> __global__ void __launch_bounds__(kClipThreads)
     int turn = 0;
     row_all<kClipThreads, AddOp>(total, &sums, turn);
     if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm) *a.norm = (float)sqrt(total[0]);
-    if constexpr (WRITE) {
-        const ClipTensor *const table = HERE ? a.here : a.table;
-        const int64_t c0 = (int64_t)blockIdx.x * a.per_wg;
-        const int c1 = (int)(c0 + a.per_wg < a.chunks ? c0 + a.per_wg : a.chunks);
-        clip_write<kClipThreads>(a, table, (int)c0, c1, clip_factor(a, total[0]));
-    }
+    if constexpr (WRITE)
+        clip_write<kClipThreads>(a, HERE ? a.here : a.table, (int)blockIdx.x, (int)gridDim.x,
+                                 clip_factor(a, total[0]));
 }
 
 // All of it by one workgroup.
@@ -181,11 +235,11 @@ template <bool HERE, bool WRITE> __global__ void __launch_bounds__(kClipOneThrea
 {
     __shared__ RowSums<kClipOneThreads> sums;
     const ClipTensor *const table = HERE ? a.here : a.table;
-    double total[1] = {clip_squares<kClipOneThreads>(a, table, 0, a.chunks)};
+    double total[1] = {clip_squares<kClipOneThreads>(a, table, 0, 1)};
     int turn = 0;
     row_all<kClipOneThreads, AddOp>(total, &sums, turn);
     if (threadIdx.x == 0 && a.norm) *a.norm = (float)sqrt(total[0]);
-    if constexpr (WRITE) clip_write<kClipOneThreads>(a, table, 0, a.chunks, clip_factor(a, total[0]));
+    if constexpr (WRITE) clip_write<kClipOneThreads>(a, table, 0, 1, clip_factor(a, total[0]));
 }
 
 // A part of a table that is too long for a launch, to the workspace.

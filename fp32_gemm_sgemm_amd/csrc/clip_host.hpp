@@ -157,8 +157,7 @@ hipError_t run_clip(bool write, int count, const sgemm_tensor *tensors, float ma
         a.count = n;
         const ClipKernels &k = kClipKernels[a.table ? 1 : 0][write ? 1 : 0];
         if (chunks <= kClipOneChunks) return launch1(k.one, dim3(1), sgemm::kClipOneThreads, &a, stream);
-        a.per_wg = (int)sgemm::ceil_div_ll(chunks, sgemm::kClipMaxWgs);
-        a.parts = (int)sgemm::ceil_div_ll(chunks, a.per_wg);
+        a.parts = chunks < sgemm::kClipMaxWgs ? (int)chunks : sgemm::kClipMaxWgs;
         const hipError_t e = launch1(k.norm, dim3((unsigned)a.parts), sgemm::kClipThreads, &a, stream);
         if (e != hipSuccess) return e;
         return launch1(k.scale, dim3(write ? (unsigned)a.parts : 1u), sgemm::kClipThreads, &a, stream);
