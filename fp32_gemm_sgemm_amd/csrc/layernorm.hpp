@@ -7,20 +7,21 @@
 //
 // Like the RMS norm (rowops.hpp, whose forms by row length these kernels take)
 // they are bound by memory and make one pass: a row stays in the registers of
-// one wave or one workgroup.  Unlike it, the squares need the mean first, so a
-// row costs two reductions (and the 8-bit form a third, as the largest |Y| is
-// not a multiple of r once b is added).  The mean is summed in float64 from the
-// start and kept in two float32 parts, so that a row whose mean is far from
-// zero loses nothing but its own representation: d is S - m to a rounding or two.
-// Longer rows are read twice (8-bit: three times); their sums are taken about the row's
-// first value x0 in float64, mean(d^2) = mean((S - x0)^2) - (m - x0)^2, where
-// the difference cancels by a factor of D at most, as the first value itself
-// adds (m - x0)^2 / D to the mean of the squares.
+// one wave or one workgroup.  Mean and variance come from one reduction: sums
+// of e = S - x0 and of e^2 in float64, x0 the row's first value, with
 //
-// A code is that of Y / scale in float64 (which the vector unit computes at
-// float32's rate), rounded to float32 and then to 8 bits, so that next to the
-// border of two codes it goes the formula's way but for the rounding of S.  The
-// forward's squares are float64 too, so they cannot overflow.
+//   m = x0 + mean(e),  var = mean(e^2) - mean(e)^2,
+//
+// where the difference cancels by a factor of D at most, as the first value
+// itself adds (m - x0)^2 / D to the variance: what is lost of float64's 53 bits
+// is log2(D), and no square overflows.  (The vector unit adds and multiplies
+// float64 at float32's rate.)  The mean is kept in two float32 parts, so that a
+// row whose mean is far from zero loses nothing but its own representation.
+//
+// A code is that of Y / scale in float64, rounded to float32 and then to 8 bits,
+// so that next to the border of two codes it goes the formula's way but for the
+// rounding of S.  It needs a second reduction, as the largest |Y| is not a
+// multiple of r once b is added.
 #pragma once
 
 #include "common.hpp"
@@ -99,23 +100,24 @@ template <typename Op, typename T> __device__ __forceinline__ T wave_all(T x)
 // barrier a reduction is enough (a half is written again two reductions later).
 template <int NT> struct RowSums {
     static constexpr int kWaves = NT / 64;
-    double v[2][3 * kWaves];
+    double v[2][4 * kWaves];
 };
 
 // N values combined over the NT threads that share a row.
 template <int NT, typename Op, typename T, int N>
 __device__ __forceinline__ void row_all(T (&x)[N], RowSums<NT> *sums, int &turn)
 {
-    static_assert(N <= 3, "room for three values a wave");
+    static_assert(N <= 4, "room for four values a wave");
     const Op op;
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = wave_all<Op>(x[i]);
     if constexpr (NT > 64) {
         constexpr int W = NT / 64;
+        static_assert(W == 4 || W == 8 || W == 16, "waves of a workgroup");
         T *const v = reinterpret_cast<T *>(sums->v[turn]);
         if constexpr (kLdsPoison) {
             float *const f = reinterpret_cast<float *>(sums->v[turn]);
-            if (threadIdx.x < 6 * W) lds_poison(f + threadIdx.x, 1);
+            if (threadIdx.x < 8 * W) lds_poison(f + threadIdx.x, 1);
             lds_poison_done();
             __syncthreads();
         }
@@ -125,14 +127,29 @@ __device__ __forceinline__ void row_all(T (&x)[N], RowSums<NT> *sums, int &turn)
             for (int i = 0; i < N; ++i) v[i * W + wave] = x[i];
         }
         __syncthreads();
+        // each lane takes one wave's value (held by every thread at once they would
+        // cost 2 W registers a value) and adds the W of them across its neighbours
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] = v[i * W];
-#pragma unroll
-            for (int w = 1; w < W; ++w) x[i] = op(x[i], v[i * W + w]);
+            x[i] = v[i * W + (threadIdx.x & (W - 1))];
+            x[i] = op(x[i], dpp_lane<0xB1>(x[i]));
+            x[i] = op(x[i], dpp_lane<0x4E>(x[i]));
+            if constexpr (W >= 8) x[i] = op(x[i], dpp_lane<0x141>(x[i]));
+            if constexpr (W >= 16) x[i] = op(x[i], dpp_lane<0x140>(x[i]));
         }
         turn ^= 1;
     }
+}
+
+// 1 / sqrt(x), x > 0: the hardware's estimate and two of Newton's steps.  (The
+// compiler's division and root take four times the instructions, one after the
+// other, while a row waits.)
+__device__ __forceinline__ double inv_sqrt(double x)
+{
+    double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = y * __builtin_fma(-0.5 * x * y, y, 1.5);
+    return y;
 }
 
 // A mean in two float32 parts.
@@ -159,6 +176,25 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_kernel(LnArgs a
     const int t = RPB == 1 ? threadIdx.x : threadIdx.x & 63;
     const int sub = RPB == 1 ? 0 : threadIdx.x >> 6;
     const int D = a.D;
+    const double inv_d = 1.0 / D;
+    // Q8: w and b of this thread's columns, for all its rows (read in every row, as
+    // the float32 form does, each group is waited for twice: 8192 x 8192 with
+    // residual 219 us against 180)
+    constexpr int VR = V > 0 && Q8 ? V : 1;
+    float wr[VR][4], br[VR][4];
+    if constexpr (V > 0 && Q8) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int col = 4 * (i * NT + t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wr[i][j] = col + j < D ? 1.0f : 0.0f;
+                br[i][j] = 0.0f;
+            }
+            if (a.w && col < D) load_cols<4>(a.w + col, col, D, wr[i]);
+            if (a.b && col < D) load_cols<4>(a.b + col, col, D, br[i]);
+        }
+    }
     int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * RPB + sub; row < a.rows; row += (int64_t)gridDim.x * RPB) {
         const float *x = a.X + row * a.ldx;
@@ -174,44 +210,47 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_kernel(LnArgs a
                 for (int j = 0; j < 4; ++j) s[j] += q[j];
             }
         };
-        // Y of one group: from d, or from S in float64
+        // (bases that the compiler takes for this row's own: it would keep w's and
+        // b's addresses for every group in vector registers from row to row)
+        const float *wp = a.w, *bp = a.b;
+        asm volatile("" : "+s"(wp), "+s"(bp));
         auto affine = [&](int col, float (&w)[4], float (&b)[4]) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 w[j] = 1.0f;
                 b[j] = 0.0f;
             }
-            if (a.w) load_cols<4>(a.w + col, col, D, w);
-            if (a.b) load_cols<4>(a.b + col, col, D, b);
+            if (wp) load_cols<4>(wp + col, col, D, w);
+            if (bp) load_cols<4>(bp + col, col, D, b);
         };
-        auto value = [&](int col, const float (&d)[4], float inv, float (&y)[4]) {
+        // Y of one group from S, in float32 and in float64
+        auto narrow = [&](int col, const float (&s)[4], const Mean &m, float inv, float (&y)[4]) {
             float w[4], b[4];
             affine(col, w, b);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(d[j] * inv, w[j], b[j]);
+            for (int j = 0; j < 4; ++j) y[j] = __builtin_fmaf(m.from(s[j]) * inv, w[j], b[j]);
         };
-        auto wide = [&](int col, const float (&s)[4], double m, double inv, double (&y)[4]) {
-            float w[4], b[4];
-            affine(col, w, b);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                y[j] = __builtin_fma(((double)s[j] - m) * inv, (double)w[j], (double)b[j]);
+        auto wide = [&](float s, double m, double inv, float w, float b) {
+            return __builtin_fma(((double)s - m) * inv, (double)w, (double)b);
         };
         // a row's scale from its largest |Y|; returns the factor from Y to its
         // code's value
         auto set_scale = [&](double big) {
-            const double scale = fmax(big / kE4m3Max, (double)kE4m3MinScale);
+            const double scale = fmax(big * (1.0 / kE4m3Max), (double)kE4m3MinScale);
             if (t == 0) a.scale[row] = (float)scale;
             return 1.0 / scale;
         };
-        auto codes = [&](int col, const double (&y)[4], double f) {
-            float c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = (float)(y[j] * f);
-            store_codes(a.Q + row * a.ldq + col, col, D, c);
+        // the mean and r of the sums of e and e^2
+        auto moments = [&](const double (&sum)[2], double x0, double &mean, double &inv) {
+            const double e = sum[0] * inv_d;
+            mean = x0 + e;
+            inv = inv_sqrt(fmax(sum[1] * inv_d - e * e, 0.0) + a.eps);
         };
 
         if constexpr (V > 0) {
+            // S is stored after the reduction's barrier: it may be X or R, whose
+            // first value every thread reads
+            const double x0 = (double)(r ? x[0] + r[0] : x[0]);
             float s[V][4];
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -220,58 +259,66 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_kernel(LnArgs a
                 for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
                 if (col < D) load_s(col, s[i]);
             }
-            double sum[1] = {0.0};
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int col = 4 * (i * NT + t);
-                if (so && col < D) store_row<4>(so + col, col, D, s[i], 1.0f, 0.0f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[0] += (double)s[i][j];
-            }
-            row_all<NT, AddOp>(sum, &sums, turn);
-            const double mean = sum[0] / D;
-            const Mean m(mean);
-            double var[1] = {0.0};
+            double sum[2] = {0.0, 0.0};
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int col = 4 * (i * NT + t);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (!Q8) s[i][j] = m.from(s[i][j]);
-                    const double d = Q8 ? (double)s[i][j] - mean : (double)s[i][j];
-                    if (col + j < D) var[0] += d * d;
+                    const double e = col + j < D ? (double)s[i][j] - x0 : 0.0;
+                    sum[0] += e;
+                    sum[1] += e * e;
                 }
             }
-            row_all<NT, AddOp>(var, &sums, turn);
-            const double inv = 1.0 / sqrt(var[0] / D + a.eps);
-            if constexpr (Q8) {
-                double y[4], big[1] = {0.0};
+            row_all<NT, AddOp>(sum, &sums, turn);
+            double mean, inv;
+            moments(sum, x0, mean, inv);
+            if (so) {
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int col = 4 * (i * NT + t);
-                    if (col >= D) continue;
-                    wide(col, s[i], mean, inv, y);
+                    if (col < D) store_row<4>(so + col, col, D, s[i], 1.0f, 0.0f);
+                }
+            }
+            if constexpr (Q8) {
+                double big[1] = {0.0};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (col + j < D) big[0] = fmax(big[0], fabs(y[j]));
+                for (int i = 0; i < V; ++i) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // (w and b are 0 past the row)
+                        const double y = fabs(wide(s[i][j], mean, inv, wr[i][j], br[i][j]));
+                        big[0] = y > big[0] ? y : big[0];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 row_all<NT, MaxOp>(big, &sums, turn);
                 const double f = set_scale(big[0]);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int col = 4 * (i * NT + t);
-                    if (col >= D) continue;
-                    wide(col, s[i], mean, inv, y);
-                    codes(col, y, f);
+                    float c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // (computed again: the compiler would keep float64 values of
+                        // all groups if it saw that they are the same)
+                        asm volatile("" : "+v"(s[i][j]));
+                        c[j] = (float)(wide(s[i][j], mean, inv, wr[i][j], br[i][j]) * f);
+                    }
+                    if (col < D) store_codes(a.Q + row * a.ldq + col, col, D, c);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             } else {
+                const Mean m(mean);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int col = 4 * (i * NT + t);
-                    if (col >= D) continue;
-                    float y[4];
-                    value(col, s[i], (float)inv, y);
-                    store_row<4>(a.Y + row * a.ldy + col, col, D, y, 1.0f, 0.0f);
+                    if (col < D) {
+                        float y[4];
+                        narrow(col, s[i], m, (float)inv, y);
+                        store_row<4>(a.Y + row * a.ldy + col, col, D, y, 1.0f, 0.0f);
+                    }
+                    asm volatile("" ::: "memory");
                 }
             }
         } else {
@@ -291,8 +338,8 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_kernel(LnArgs a
                 }
             }
             row_all<NT, AddOp>(sum, &sums, turn);
-            const double e = sum[0] / D, mean = x0 + e;
-            const double inv = 1.0 / sqrt(fmax(sum[1] / D - e * e, 0.0) + a.eps);
+            double mean, inv;
+            moments(sum, x0, mean, inv);
             // (each thread reads what it wrote itself: with S given, X and R may
             // be the memory it went to)
             auto again = [&](int col, float (&s)[4]) {
@@ -300,33 +347,35 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_kernel(LnArgs a
                 else load_s(col, s);
             };
             if constexpr (Q8) {
-                double big[1] = {0.0};
-                for (int64_t c = 4 * t; c < D; c += 4 * NT) {
-                    float s[4];
-                    double y[4];
-                    again((int)c, s);
-                    wide((int)c, s, mean, inv, y);
+                // f(column, its four values of Y) for this thread's groups
+                auto each = [&](auto f) {
+                    for (int64_t c = 4 * t; c < D; c += 4 * NT) {
+                        float s[4], w[4], b[4];
+                        double y[4];
+                        again((int)c, s);
+                        affine((int)c, w, b);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (c + j < D) big[0] = fmax(big[0], fabs(y[j]));
-                }
+                        for (int j = 0; j < 4; ++j) y[j] = wide(s[j], mean, inv, w[j], b[j]);
+                        f((int)c, y);
+                    }
+                };
+                double big[1] = {0.0};
+                each([&](int c, const double (&y)[4]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) big[0] = c + j < D && fabs(y[j]) > big[0] ? fabs(y[j]) : big[0];
+                });
                 row_all<NT, MaxOp>(big, &sums, turn);
                 const double f = set_scale(big[0]);
-                for (int64_t c = 4 * t; c < D; c += 4 * NT) {
-                    float s[4];
-                    double y[4];
-                    again((int)c, s);
-                    wide((int)c, s, mean, inv, y);
-                    codes((int)c, y, f);
-                }
+                each([&](int c, const double (&y)[4]) {
+                    const float v[4] = {(float)(y[0] * f), (float)(y[1] * f), (float)(y[2] * f), (float)(y[3] * f)};
+                    store_codes(a.Q + row * a.ldq + c, c, D, v);
+                });
             } else {
                 const Mean m(mean);
                 for (int64_t c = 4 * t; c < D; c += 4 * NT) {
                     float s[4], y[4];
                     again((int)c, s);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[j] = m.from(s[j]);
-                    value((int)c, s, (float)inv, y);
+                    narrow((int)c, s, m, (float)inv, y);
                     store_row<4>(a.Y + row * a.ldy + c, (int)c, D, y, 1.0f, 0.0f);
                 }
             }
@@ -369,6 +418,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
     const int t = RPB == 1 ? threadIdx.x : threadIdx.x & 63;
     const int sub = RPB == 1 ? 0 : threadIdx.x >> 6;
     const int D = a.D;
+    const double inv_d = 1.0 / D;
     float dw[VS][4], db[VS][4], w[VS][4];
 #pragma unroll
     for (int i = 0; i < VS; ++i) {
@@ -398,6 +448,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
             }
             store_row<4>(dx + col, col, D, o, 1.0f, 0.0f);
         };
+        const double x0 = (double)s[0];
         if constexpr (V > 0) {
             float y[VS][4], x[VS][4];
 #pragma unroll
@@ -410,46 +461,47 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
                     load_cols<4>(dy + col, col, D, y[i]);
                 }
             }
-            double sum[1] = {0.0};
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sum[0] += (double)x[i][j];
-            row_all<NT, AddOp>(sum, &sums, turn);
-            const Mean m(sum[0] / D);
-            float q[3] = {0.0f, 0.0f, 0.0f};  // d^2, g, g d
+            double q[4] = {0.0, 0.0, 0.0, 0.0};  // e, e^2, g, g e
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int col = 4 * (i * NT + t);
+                auto add = [&](int j) {
+                    const double e = (double)x[i][j] - x0, g = (double)(y[i][j] * w[i][j]);
+                    q[0] += e;
+                    q[1] += e * e;
+                    q[2] += g;
+                    q[3] += g * e;
+                };
+                if (col + 3 < D) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] = col + j < D ? m.from(x[i][j]) : 0.0f;
-                    const float g = y[i][j] * w[i][j];
-                    q[0] += x[i][j] * x[i][j];
-                    q[1] += g;
-                    q[2] += g * x[i][j];
+                    for (int j = 0; j < 4; ++j) add(j);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (col + j < D) add(j);
                 }
             }
             row_all<NT, AddOp>(q, &sums, turn);
-            const float inv_d = 1.0f / (float)D;
-            const float r = 1.0f / sqrtf(q[0] * inv_d + a.eps);
-            const float mg = q[1] * inv_d, c = q[2] * inv_d * r * r * r;
+            const double e = q[0] * inv_d, rd = inv_sqrt(fmax(q[1] * inv_d - e * e, 0.0) + a.eps);
+            const Mean m(x0 + e);
+            const float r = (float)rd, mg = (float)(q[2] * inv_d);
+            const float c = (float)((q[3] - e * q[2]) * inv_d * rd * rd * rd);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int col = 4 * (i * NT + t);
                 if (col < D) {
-                    float g[4];
+                    float g[4], d[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         g[j] = y[i][j] * w[i][j];
-                        dw[i][j] += y[i][j] * (x[i][j] * r);
+                        d[j] = m.from(x[i][j]);
+                        dw[i][j] += y[i][j] * (d[j] * r);
                         db[i][j] += y[i][j];
                     }
-                    write(col, g, x[i], r, mg, c);
+                    write(col, g, d, r, mg, c);
                 }
             }
         } else {
-            const double x0 = (double)s[0];
             auto load = [&](int col, float (&g)[4], float (&x)[4]) {
                 load_cols<4>(dy + col, col, D, g);
                 load_cols<4>(s + col, col, D, x);
@@ -460,7 +512,7 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
                     for (int j = 0; j < 4; ++j) g[j] *= u[j];
                 }
             };
-            double q[2] = {0.0, 0.0}, p[2] = {0.0, 0.0};  // e, e^2 and g, g e of e = S - x0
+            double q[4] = {0.0, 0.0, 0.0, 0.0};
             for (int64_t col = 4 * t; col < D; col += 4 * NT) {
                 float g[4], x[4];
                 load((int)col, g, x);
@@ -469,16 +521,15 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
                     const double e = col + j < D ? (double)x[j] - x0 : 0.0;
                     q[0] += e;
                     q[1] += e * e;
-                    p[0] += (double)g[j];
-                    p[1] += (double)g[j] * e;
+                    q[2] += (double)g[j];
+                    q[3] += (double)g[j] * e;
                 }
             }
             row_all<NT, AddOp>(q, &sums, turn);
-            row_all<NT, AddOp>(p, &sums, turn);
-            const double e = q[0] / D;
+            const double e = q[0] * inv_d, rd = inv_sqrt(fmax(q[1] * inv_d - e * e, 0.0) + a.eps);
             const Mean m(x0 + e);
-            const double rd = 1.0 / sqrt(fmax(q[1] / D - e * e, 0.0) + a.eps);
-            const float r = (float)rd, mg = (float)(p[0] / D), c = (float)((p[1] - e * p[0]) / D * rd * rd * rd);
+            const float r = (float)rd, mg = (float)(q[2] * inv_d);
+            const float c = (float)((q[3] - e * q[2]) * inv_d * rd * rd * rd);
             for (int64_t col = 4 * t; col < D; col += 4 * NT) {
                 float g[4], x[4];
                 load((int)col, g, x);

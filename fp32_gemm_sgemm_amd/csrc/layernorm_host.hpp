@@ -30,6 +30,26 @@ bool pieces_overlap_any(const Piece &a, const Piece *others, int n)
     return false;
 }
 
+// The forms of a layer norm to 8 bits are row_form's: it holds w and b in
+// registers too, so workgroups of 512 for long rows would hold 32 values a thread
+// and be one to a compute unit as those of 1024 are (8192 x 8192 with residual:
+// 204 us against 180).
+RowForm layernorm_form(bool q8, int D, int rows, bool residual)
+{
+    return q8 ? row_form(D) : row_form_forward(D, rows, residual);
+}
+
+// Workgroups of a layer norm: to 8 bits as many as share the chip, which then
+// loop over the rows with w and b in their registers (microseconds with
+// residual, so many and one a row: 8192 x 4096 80 and 118, 8192 x 8192 180 and 202,
+// 4096 x 16384 204 and 239).
+long long layernorm_wgs(bool q8, const RowForm &f)
+{
+    if (!q8 || f.v == 0) return 0;
+    if (f.nt == 1024) return f.v == 2 ? 512 : 256;
+    return f.v == 4 ? 768 : 2048;
+}
+
 template <bool Q8> const void *layernorm_kernel_for(const RowForm &f)
 {
     using sgemm::layernorm_kernel;
@@ -42,10 +62,11 @@ template <bool Q8> const void *layernorm_kernel_for(const RowForm &f)
         if (f.v == 2) return reinterpret_cast<const void *>(&layernorm_kernel<256, 2, Q8>);
         return reinterpret_cast<const void *>(&layernorm_kernel<256, 4, Q8>);
     }
-    if (f.nt == 512) {
-        if (f.v == 4) return reinterpret_cast<const void *>(&layernorm_kernel<512, 4, Q8>);
-        return reinterpret_cast<const void *>(&layernorm_kernel<512, 8, Q8>);
-    }
+    if constexpr (!Q8)
+        if (f.nt == 512) {
+            if (f.v == 4) return reinterpret_cast<const void *>(&layernorm_kernel<512, 4, Q8>);
+            return reinterpret_cast<const void *>(&layernorm_kernel<512, 8, Q8>);
+        }
     if (f.v == 2) return reinterpret_cast<const void *>(&layernorm_kernel<1024, 2, Q8>);
     if (f.v == 4) return reinterpret_cast<const void *>(&layernorm_kernel<1024, 4, Q8>);
     return reinterpret_cast<const void *>(&layernorm_kernel<1024, 0, Q8>);
@@ -111,9 +132,9 @@ hipError_t run_layernorm(bool q8, int rows, int D, const float *X, int ldx, cons
     a.rows = rows;
     a.D = D;
     a.eps = eps;
-    const RowForm f = row_form_forward(D, rows, R != nullptr);
-    return launch1(q8 ? layernorm_kernel_for<true>(f) : layernorm_kernel_for<false>(f), dim3(row_grid(f, rows, 0)),
-                   f.nt > 256 ? f.nt : 256, &a, stream);
+    const RowForm f = layernorm_form(q8, D, rows, R != nullptr);
+    return launch1(q8 ? layernorm_kernel_for<true>(f) : layernorm_kernel_for<false>(f),
+                   dim3(row_grid(f, rows, layernorm_wgs(q8, f))), f.nt > 256 ? f.nt : 256, &a, stream);
 }
 
 // ---- gradient --------------------------------------------------------------------------
@@ -137,11 +158,24 @@ hipError_t launch_pair_sum(const float *part, int parts, int N, float *first, fl
 // Bytes of every row's mean and r (16-byte padded), for the column pass of long rows.
 size_t layernorm_rows_bytes(int rows) { return ((size_t)rows * sizeof(sgemm::LnRow) + 15) & ~(size_t)15; }
 
+// Workgroups of the one-pass form with sums: four rows or more each, as for the RMS
+// norm's gradient, but at least 512 where there are so many rows, and at most as
+// many as share the chip, since each writes 2 D sums (microseconds, without their
+// sum: 8192 x 4096 with 768 and 1024 workgroups 100 and 105, 8192 x 8192 with
+// 256 and 1024 143 and 155, 515 x 2052 with 256 and 515 9.8 and 7.6).
+long long layernorm_grad_wgs(const RowForm &f, int rows)
+{
+    const long long at_once = f.nt >= 256 ? 1 : 256 / f.nt;
+    const long long n = sgemm::ceil_div_ll(rows, 4 * at_once), most = f.nt == 1024 ? 256 : f.v == 4 ? 768 : 1024;
+    const long long least = most < 512 ? most : 512;
+    return n < least ? least : n < most ? n : most;
+}
+
 // Workspace of the sums: each workgroup's (or chunk's) 2 D partial ones.
 size_t layernorm_grad_bytes(int rows, int D)
 {
     const RowForm f = row_form(D);
-    if (f.v > 0) return (size_t)row_grid(f, rows, row_grad_wgs(f, rows)) * 8u * (size_t)D;
+    if (f.v > 0) return (size_t)row_grid(f, rows, layernorm_grad_wgs(f, rows)) * 8u * (size_t)D;
     return layernorm_rows_bytes(rows) + (size_t)col_plan(rows, D).chunks * 8u * (size_t)D;
 }
 
@@ -190,7 +224,7 @@ hipError_t run_layernorm_grad(int rows, int D, const float *dY, int ldy, const f
     a.rows = rows;
     a.D = D;
     a.eps = eps;
-    const unsigned grid = row_grid(f, rows, sums && f.v > 0 ? row_grad_wgs(f, rows) : 0);
+    const unsigned grid = row_grid(f, rows, sums && f.v > 0 ? layernorm_grad_wgs(f, rows) : 0);
     char *const at = static_cast<char *>(ws);
     if (sums && f.v > 0) a.part = reinterpret_cast<float *>(at);
     if (sums && f.v == 0) a.rows3 = reinterpret_cast<sgemm::LnRow *>(at);
