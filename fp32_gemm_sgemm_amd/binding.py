@@ -139,6 +139,8 @@ def load(path=None):
         "sgemm_f32_gated_workspace": [i, i, i, i, p, i, p, i, p, i, ctypes.POINTER(sz)],
         "sgemm_e4m3_gated": [i, i, i, p, i, p, p, i, p, p, i, p, p, i, ctypes.POINTER(SgemmGate), p, sz, p],
         "sgemm_e4m3_gated_workspace": [i, i, i, ctypes.POINTER(sz)],
+        "sgemm_f32_pair": [i, i, i, i, p, p, i, p, i, p, i, p, i, p, sz, p],
+        "sgemm_f32_pair_workspace": [i, i, i, i, p, p, i, p, i, p, i, ctypes.POINTER(sz)],
         "sgemm_f32_gated_grad": [i, i, i, p, i, p, i, p, i, p, i, p, i, p, p, p, sz, p],
         "sgemm_f32_gated_grad_workspace": [i, i, ctypes.POINTER(sz)],
         "sgemm_layernorm_f32": [i, i, p, i, p, i, p, p, f, p, i, p, i, p],

@@ -149,16 +149,32 @@ sgemm::Problem gated_problem(const GatedCall &c)
                           (int)sgemm::partial_ld(c.N), gated_batch(c) ? 2 : 1};
 }
 
-// Streaming rate of the form for few rows, and its cost beyond the stream.
-constexpr double kGatedRowsBytesPerNs = 4800.0;
-constexpr double kGatedRowsNs = 2000.0;
+// The form for few rows, without the launch that every form pays: its cost beyond the
+// stream, and the stream's rate over the chip, a share of it slower for each row past
+// the first, and for weights stored (K, N) by the workgroups (32 columns each) there
+// are.  Measured (microseconds, launch included), 1, 2 and 4 rows: 26.6, 28.0 and
+// 30.0 for weights of 8192 x 2048 stored (N, K), 29.1 and 30.6 (1 and 4) stored
+// (K, N); 65.6 for one row of 2048 x 8192 stored so, 64 workgroups, against 22.5.
+// With more rows the fixed cost is paid by every round of workgroups: 45 rows of
+// 2048 x 84, 11.4; 25 rows of 2371 x 163 stored (K, N), 25.1.
+constexpr double kGatedRowsNs = 2000.0, kGatedRowsNsXc = 5000.0;
+constexpr int kGatedRowsPerCu = 4, kGatedRowsPerCuXc = 1;  // workgroups that share a compute unit
+constexpr double kGatedRowsBytesPerNs = 6300.0, kGatedRowsBytesPerNsXc = 5600.0, kGatedRowsWgBytesPerNsXc = 36.0;
+constexpr double kGatedRowsPerRow = 0.05;
 // The second pass that two products need (its launch, and the wait for the
 // first ones).
 constexpr double kGateReduceNs = 5000.0;
 
-double gated_rows_ns(const GatedCall &c)
+double gated_rows_ns(const GatedCall &c, int cus)
 {
-    return kGatedRowsNs + (double)sgemm::ceil_div_ll(c.M, sgemm::kGatedRows) * 8.0 * c.K * (double)c.N / kGatedRowsBytesPerNs;
+    const long long blocks = sgemm::ceil_div_ll(c.M, sgemm::kGatedRows);
+    const double rows = c.M < sgemm::kGatedRows ? c.M : sgemm::kGatedRows;
+    const long long wgs = blocks * sgemm::ceil_div_ll(c.N, c.transb ? 8 : 32);
+    const double rate = c.transb ? kGatedRowsBytesPerNs
+                                 : std::min(kGatedRowsBytesPerNsXc, kGatedRowsWgBytesPerNsXc * (double)wgs);
+    const double fixed = c.transb ? kGatedRowsNs * (double)sgemm::ceil_div_ll(wgs, kGatedRowsPerCu * (long long)cus)
+                                  : kGatedRowsNsXc * (double)sgemm::ceil_div_ll(wgs, kGatedRowsPerCuXc * (long long)cus);
+    return fixed + (double)blocks * 8.0 * c.K * (double)c.N * (1.0 + kGatedRowsPerRow * (rows - 1.0)) / rate;
 }
 
 double gated_tile_ns(const GatedTile &v, const GatedCall &c, int cus)
@@ -204,7 +220,7 @@ GatedPlan gated_products_plan(const GatedCall &c, int cus, long long ws, double 
 GatedPlan gated_plan(const GatedCall &c, int cus, long long ws)
 {
     GatedPlan best = {SGEMM_GATED_ROWS, {-1, 1, 0, 0}, 0};
-    double best_t = gated_rows_ns(c);
+    double best_t = gated_rows_ns(c, cus);
     const bool aligned = gated_aligned16(c);
     for (int i = 0; i < kGatedTileCount; ++i) {
         const GatedTile &v = kGatedTiles[i];
@@ -420,6 +436,91 @@ hipError_t run_gated(int transb, int M, int N, int K, const float *A, int lda, c
     if (plan.form < kGatedTileCount) return launch_gated_tile(kGatedTiles[plan.form], c, e, stream);
     if (plan.form == SGEMM_GATED_ROWS) return launch_gated_rows(c, e, cus, stream);
     return launch_gated_products(c, plan, e, stream);
+}
+
+// ---- the sum of two products ------------------------------------------------------------
+
+// C = A1 op(B1) + A2 op(B2): as one batch of two whose partial products (and
+// those of a K split) are added by one reduction, or one product after the other,
+// the second added to the first's result.  The batch has twice the tiles, which
+// pays where one product does not fill the chip.
+struct PairCall {
+    Call c[2];  // as the product's entry takes them, the second with beta 1
+};
+
+struct PairPlan {
+    bool batch;
+    sgemm::Choice choice;  // of the batch
+    long long workspace_bytes;
+};
+
+// The batch's problem (its partials as the workspace holds them).
+sgemm::Problem pair_problem(const PairCall &p)
+{
+    sgemm::Problem q = p.c[0].p;
+    q.batch = 2;
+    q.ldc = (int)sgemm::partial_ld(q.N);
+    return q;
+}
+
+PairPlan pair_plan(const PairCall &p, int cus, long long ws)
+{
+    const sgemm::Problem &one = p.c[0].p, two = pair_problem(p);
+    const bool aligned = rows_aligned16(p.c[0]) && rows_aligned16(p.c[1]), lds_ok = sgemm::direct_lds_ok(one);
+    double t1 = 0.0, t2 = 0.0;
+    const sgemm::Choice ch = sgemm::select_plan(kVariants, kNumVariants, one, cus, aligned, lds_ok, ws, false, true, &t1);
+    PairPlan plan = {false, {-1, 1, 0, 0}, ch.id < 0 ? 0 : sgemm::split_workspace_bytes(
+                     sgemm::main_block(one, ch.strip_m, ch.strip_n), ch.splits)};
+    if (gate_parts_bytes(one.M, one.N, 1) > ws || one.ldb != p.c[1].p.ldb || one.lda != p.c[1].p.lda) return plan;
+    const sgemm::Choice both = sgemm::select_plan(kVariants, kNumVariants, two, cus, aligned, lds_ok, ws, false, false, &t2);
+    const long long bytes = gate_parts_bytes(one.M, one.N, both.splits);
+    if (both.id < 0 || bytes > ws) return plan;
+    // (a split's reduction is in its time; it writes one sum here, not two)
+    if (both.splits <= 1) t2 += sgemm::kReduceFixedNs + 12.0 * (double)one.M * (double)one.N / sgemm::kReduceBytesPerNs;
+    if (ch.id < 0 || t2 < 2.0 * t1 + sgemm::kLaunchFloorNs) plan = {true, both, bytes};
+    return plan;
+}
+
+hipError_t run_pair(PairCall &p, hipStream_t stream)
+{
+    for (const Call &c : p.c) {
+        const hipError_t e = validate(c);
+        if (e != hipSuccess) return e;
+    }
+    const sgemm::Problem &one = p.c[0].p;
+    if (one.M == 0 || one.N == 0) return hipSuccess;
+    if (one.K == 0) return (hipError_t)run(p.c[0], stream, nullptr);
+    int cus = 0;
+    hipError_t e = device_cus(&cus);
+    if (e != hipSuccess) return e;
+    const PairPlan plan =
+        pair_plan(p, cus, p.c[0].ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)p.c[0].ws_bytes);
+    if (!plan.batch) {
+        for (const Call &c : p.c) {
+            e = (hipError_t)run(c, stream, nullptr);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    Call both = p.c[0];
+    both.p = pair_problem(p);
+    both.sa = (long long)((intptr_t)p.c[1].A - (intptr_t)p.c[0].A) / 4;
+    both.sb = (long long)((intptr_t)p.c[1].B - (intptr_t)p.c[0].B) / 4;
+    both.C = static_cast<float *>(both.ws);
+    both.sc = (long long)one.M * both.p.ldc;
+    sgemm_cfg cfg;
+    const Variant &v = kVariants[plan.choice.id];
+    if (!sgemm::finish_cfg(v, plan.choice.id, both.p, plan.choice.splits, 0, 0, &cfg)) return hipErrorInvalidValue;
+    e = launch_gemm(v, cfg, both, stream);
+    // (the partial sums of both products lie one after the other)
+    return e == hipSuccess ? launch_reduce(p.c[0], 2 * cfg.splits, 1.0f, stream) : e;
+}
+
+PairCall make_pair(int transb, int M, int N, int K, const float *A1, const float *A2, int lda, const float *B1, int ldb1,
+                   const float *B2, int ldb2, float *C, int ldc, void *ws, size_t ws_bytes)
+{
+    return {{make_call(0, transb, M, N, K, 1.0f, A1, lda, 0, B1, ldb1, 0, 0.0f, C, ldc, 0, 1, ws, ws_bytes),
+             make_call(0, transb, M, N, K, 1.0f, A2, lda, 0, B2, ldb2, 0, 1.0f, C, ldc, 0, 1, ws, ws_bytes)}};
 }
 
 // ---- 8 bits ---------------------------------------------------------------------------------

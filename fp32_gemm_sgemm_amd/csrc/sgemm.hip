@@ -1040,6 +1040,28 @@ int sgemm_f32_gated_workspace(int transb, int M, int N, int K, const float *A, i
     return hipSuccess;
 }
 
+int sgemm_f32_pair(int transb, int M, int N, int K, const float *A1, const float *A2, int lda, const float *B1, int ldb1,
+                   const float *B2, int ldb2, float *C, int ldc, void *workspace, size_t workspace_bytes,
+                   hipStream_t stream)
+{
+    PairCall p = make_pair(transb, M, N, K, A1, A2, lda, B1, ldb1, B2, ldb2, C, ldc, workspace, workspace_bytes);
+    return run_pair(p, stream);
+}
+
+int sgemm_f32_pair_workspace(int transb, int M, int N, int K, const float *A1, const float *A2, int lda, const float *B1,
+                             int ldb1, const float *B2, int ldb2, size_t *bytes)
+{
+    const PairCall p = make_pair(transb, M, N, K, A1, A2, lda, B1, ldb1, B2, ldb2, nullptr, N > 1 ? N : 1, nullptr, 0);
+    if (!bytes || !sgemm::sizes_ok(p.c[0].p) || !sgemm::sizes_ok(p.c[1].p)) return hipErrorInvalidValue;
+    *bytes = 0;
+    if (M == 0 || N == 0 || K == 0) return hipSuccess;
+    int cus = 0;
+    const hipError_t e = device_cus(&cus);
+    if (e != hipSuccess) return e;
+    *bytes = (size_t)pair_plan(p, cus, LLONG_MAX).workspace_bytes;
+    return hipSuccess;
+}
+
 int sgemm_e4m3_gated(int M, int N, int K, const void *A, int lda, const float *scale_a, const void *B_gate,
                      int ldb_gate, const float *scale_gate, const void *B_up, int ldb_up, const float *scale_up,
                      float *C, int ldc, const sgemm_gate *gate, void *workspace, size_t workspace_bytes,

@@ -147,6 +147,22 @@ def _products(batch, ta, tb, M, N, K, x, ldx, sx, y, ldy, sy, beta, out, ldo, so
     _check(code, "sgemm_f32_ex")
 
 
+def _pair(tb, M, N, K, x1, x2, ldx, y1, ldy1, y2, ldy2, out, ldo, workspace, device):
+    """out = X1 op(Y1) + X2 op(Y2) of checked operands' addresses."""
+    operands = (tb, M, N, K, x1, x2, ldx, y1, ldy1, y2, ldy2)
+    ws, ws_ptr, ws_bytes = None, None, 0
+    if isinstance(workspace, _torch().Tensor):
+        ws_ptr, ws_bytes = _supplied(workspace, device)
+    elif workspace:
+        nbytes = ctypes.c_size_t(0)
+        _check(load().sgemm_f32_pair_workspace(*operands, ctypes.byref(nbytes)), "sgemm_f32_pair_workspace")
+        ws_bytes = nbytes.value
+        ws, ws_ptr = _scratch(ws_bytes, device)
+    code = load().sgemm_f32_pair(*operands, out, ldo, ws_ptr, ws_bytes, _handle(device))
+    del ws
+    _check(code, "sgemm_f32_pair")
+
+
 def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation="silu", transb=False,
                          need=("A", "B", "bias"), workspace=True, stream=None):
     """Gradients of y = act(A @ op(B_gate) + bias_gate) * (A @ op(B_up) + bias_up)
@@ -192,9 +208,8 @@ def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation=
             _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, B_gate.data_ptr(), ldg, 0, 0.0, dA.data_ptr(), max(K, 1), 0,
                       workspace, device)
         else:
-            for i, (b, ldb) in enumerate(((B_gate, ldg), (B_up, ldu))):
-                _products(1, 0, 1 - tb, M, K, N, z + 4 * half * i, ld, 0, b.data_ptr(), ldb, 0, float(i),
-                          dA.data_ptr(), max(K, 1), 0, workspace, device)
+            _pair(1 - tb, M, K, N, z, z + 4 * half, ld, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu, dA.data_ptr(),
+                  max(K, 1), workspace, device)
     if "B" in need:
         if transb:
             dB = _empty((2, N, K), device)

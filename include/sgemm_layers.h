@@ -4,8 +4,8 @@
  *
  *   - the gated feed-forward block, both projections, the activation and the
  *     product in one call, in float32 and for 8-bit operands, and the
- *     elementwise part of its gradient (sgemm_f32_gated, sgemm_e4m3_gated,
- *     sgemm_f32_gated_grad);
+ *     parts of its gradient (sgemm_f32_gated, sgemm_e4m3_gated,
+ *     sgemm_f32_gated_grad, sgemm_f32_pair);
  *   - the layer norm with the residual's addition, its output in float32 or in
  *     8 bits with one scale a row, and its gradient (sgemm_layernorm_f32,
  *     sgemm_layernorm_e4m3, sgemm_layernorm_f32_grad);
@@ -124,6 +124,26 @@ int sgemm_f32_gated_grad(int M, int N, int activation, const float *dY, int ldy,
 int sgemm_f32_gated_grad_workspace(int M, int N, size_t *bytes);
 
 /*
+ * sgemm_f32_pair: C = A1 x op(B1) + A2 x op(B2) in float32, such as the
+ * gradient that goes on from a gated block, dA = dG x op(B_gate)^T + dU x
+ * op(B_up)^T.  A1 and A2 are M x K with one row stride; B1 and B2 are K x N, or
+ * N x K with transb.
+ *
+ *   workspace  optional (16-byte aligned; NULL with 0 bytes for none): lets the
+ *            two run together, and with K split over workgroups.  The
+ *            library's wish for these very operands (they are not read) is
+ *            sgemm_f32_pair_workspace's.
+ * Limits, errors and edge cases as sgemm_f32_ex (sgemm.h).
+ */
+int sgemm_f32_pair(int transb, int M, int N, int K,
+                   const float *A1, const float *A2, int lda,
+                   const float *B1, int ldb1, const float *B2, int ldb2, float *C, int ldc,
+                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+int sgemm_f32_pair_workspace(int transb, int M, int N, int K,
+                             const float *A1, const float *A2, int lda,
+                             const float *B1, int ldb1, const float *B2, int ldb2, size_t *bytes);
+
+/*
  * sgemm_layernorm_f32: per row of D values,
  *
  *   S = X + R,   Y = (S - mean(S)) / sqrt(var(S) + eps) * w + b,
@@ -145,8 +165,8 @@ int sgemm_layernorm_f32(int rows, int D, const float *X, int ldx, const float *R
                         hipStream_t stream);
 
 /* sgemm_layernorm_e4m3: the same with the output in 8 bits and one float32
- * scale a row, as sgemm_rmsnorm_e4m3 (Y / scale is float64 up to the
- * rounding to a code). */
+ * scale a row, as sgemm_rmsnorm_e4m3 (Y / scale is float64 from S up to
+ * the rounding to a code). */
 int sgemm_layernorm_e4m3(int rows, int D, const float *X, int ldx, const float *R, int ldr,
                          const float *w, const float *b, float eps, float *S, int lds,
                          void *Q, int ldq, float *scale, hipStream_t stream);
@@ -167,8 +187,7 @@ int sgemm_layernorm_e4m3(int rows, int D, const float *X, int ldx, const float *
  *   workspace  16-byte aligned, at least what
  *           sgemm_layernorm_f32_grad_workspace gives; NULL with 0 bytes where
  *           dw and db are NULL.  Too little is refused.
- * The mean is summed in float64, everything else in float32 (rows past 16384
- * values in float64): a |d| above 1.8e19 overflows (dX is then dS, or NaN).
+ * A row's sums are float64, the sums over rows float32.
  * Other arguments as sgemm_layernorm_f32.
  */
 int sgemm_layernorm_f32_grad(int rows, int D, const float *dY, int ldy, const float *S, int lds,

@@ -34,7 +34,7 @@ def declared():
 def test_declared_functions_are_exported(lib, path):
     out = subprocess.run(["nm", "-D", "--defined-only", path], capture_output=True, text=True, check=True).stdout
     names = {line.split()[-1] for line in out.splitlines() if line.strip()}
-    assert len(declared()) == 13 and set(declared()) <= names
+    assert len(declared()) == 15 and set(declared()) <= names
 
 
 def layout(struct, name):
@@ -148,6 +148,23 @@ def test_gated_blocks_refused(lib):
     assert lib.sgemm_f32_gated_workspace(1, 8, 8, 8, P, 8, P, 8, P, 7, ctypes.byref(n)) == INVALID
     assert lib.sgemm_e4m3_gated_workspace(1, 1, -1, ctypes.byref(n)) == INVALID
     assert lib.sgemm_e4m3_gated_workspace(1, 1, 1, None) == INVALID
+
+
+def pair(lib, tb=0, M=8, N=8, K=8, A1=P, A2=2 * P, lda=8, B1=3 * P, ldb1=8, B2=4 * P, ldb2=8, C=5 * P, ldc=8, ws=0,
+         ws_bytes=0):
+    return lib.sgemm_f32_pair(tb, M, N, K, A1, A2, lda, B1, ldb1, B2, ldb2, C, ldc, ws, ws_bytes, 0)
+
+
+def test_pairs_refused(lib):
+    for kw in (dict(tb=2), dict(M=-1), dict(N=-1), dict(K=-1), dict(lda=7), dict(ldb1=7), dict(ldb2=7), dict(ldc=7), dict(A1=0),
+               dict(A2=0), dict(B1=0), dict(B2=0), dict(C=0), dict(A2=2 * P + 2), dict(B2=4 * P + 1), dict(C=5 * P + 2),
+               dict(C=P), dict(C=2 * P), dict(C=3 * P), dict(C=4 * P), dict(ws=5 * P, ws_bytes=64), dict(ws=2 * P, ws_bytes=64),
+               dict(ws=4 * P, ws_bytes=64), dict(ws=6 * P + 4, ws_bytes=64), dict(ldb2=2 ** 31 - 1)):
+        assert pair(lib, **kw) == INVALID, kw
+    assert pair(lib, M=0, A1=0, A2=0, B1=0, B2=0, C=0) == 0
+    n = ctypes.c_size_t()
+    assert lib.sgemm_f32_pair_workspace(0, 8, 8, 8, P, P, 7, P, 8, P, 8, ctypes.byref(n)) == INVALID
+    assert lib.sgemm_f32_pair_workspace(0, 8, 8, 8, P, P, 8, P, 8, P, 8, None) == INVALID
 
 
 def gate_grad(lib, M=40, N=8, act=4, dY=P, ldy=8, G=2 * P, ldg=8, U=3 * P, ldu=8, dG=4 * P, lddg=8, dU=5 * P, lddu=8, bg=6 * P,
