@@ -59,7 +59,8 @@ __device__ __forceinline__ void gate_apply(const Gate &e, int row, int col, int 
 // row0 + RS * rr of C, the first column is col0.  As in StagedEpi the
 // activation's code stands once, in a rolled loop, and every access to memory
 // is 16 bytes a lane along a row; nothing but the columns' biases and scales is
-// read, so no store is waited for.
+// read, so no store is waited for.  Without C only pre_gate and pre_up are
+// written (the partial sums of a K split).
 template <int R, int WT, int RS, bool SCALES> struct StagedGate {
     static constexpr int QR = WT / 4;     // 16-byte groups per row
     static constexpr int STEP = 64 / QR;  // rows a wave covers at once
@@ -129,6 +130,7 @@ template <int R, int WT, int RS, bool SCALES> struct StagedGate {
             const bool in = row < M && col() < N;
             if (in && e.pre_gate) write(e.pre_gate + row * e.ld_pre_gate + col(), g);
             if (in && e.pre_up) write(e.pre_up + row * e.ld_pre_up + col(), u);
+            if (!C) continue;
             epi_map<false>(e.act, g);
             if (in) write(C + row * ldc + col(), g * u);
         }

@@ -83,17 +83,20 @@ long long gate_parts_bytes(int M, int N, int splits) { return 8ll * splits * M *
 
 // The fused tiles: bm x bn of work, bm x bn / 2 outputs.  Their main loops are
 // those of the plain product's tiles of the same size (kVariants 4, 7, 20 and
-// with 4-byte loads 19, 13, 21), and so are the rates and fixed costs.
+// with 4-byte loads 19, 13, 21), and so are the rates and fixed costs.  Two
+// workgroups of the smaller ones share a compute unit and pay their fixed costs
+// together (1472 x 1790 x 500, microseconds, launch included, model and measured: 60
+// and 59 on 64x64 tiles, 66 and 66 on 128x128).
 struct GatedTile {
     int bm, bn, bk;
     bool dword;  // 4-byte loads: rows that do not start 16-byte aligned
-    int threads, eff_permille, eff_one_permille, fixed_ns;
+    int threads, eff_permille, eff_one_permille, fixed_ns, coresident;
     const void *fn[2];  // by transb
 };
 template <int BM, int BN, int BK, int WM, int WN, int ST, bool DW, int MB>
 GatedTile gated_tile(int eff, int eff_one, int fixed_ns)
 {
-    return {BM, BN, BK, DW, WM * WN * 64, eff, eff_one, fixed_ns,
+    return {BM, BN, BK, DW, WM * WN * 64, eff, eff_one, fixed_ns, BM < 256 ? 2 : 1,
             {reinterpret_cast<const void *>(&sgemm::sgemm_gated_kernel<BM, BN, BK, WM, WN, ST, false, DW, MB>),
              reinterpret_cast<const void *>(&sgemm::sgemm_gated_kernel<BM, BN, BK, WM, WN, ST, true, DW, MB>)}};
 }
@@ -182,7 +185,8 @@ double gated_tile_ns(const GatedTile &v, const GatedCall &c, int cus)
     const long long tiles = sgemm::ceil_div_ll(c.M, v.bm) * sgemm::ceil_div_ll(c.N, v.bn / 2);
     const double eff = (tiles <= cus ? v.eff_one_permille : v.eff_permille) / 1000.0;
     const double slice_ns = 2.0 * v.bm * v.bn * v.bk / (sgemm::kCuFlopPerNs * eff);
-    return (double)sgemm::ceil_div_ll(tiles, cus) * (v.fixed_ns + (double)sgemm::ceil_div_ll(c.K, v.bk) * slice_ns);
+    return (double)sgemm::ceil_div_ll(tiles, (long long)cus * v.coresident) * v.fixed_ns +
+           (double)sgemm::ceil_div_ll(tiles, cus) * (double)sgemm::ceil_div_ll(c.K, v.bk) * slice_ns;
 }
 
 // Whether a tile can serve the call: offsets in 32 bits, and a grid that a launch counts.
@@ -547,26 +551,20 @@ const E4m3SkinnyKernel kE4m3GatedSkinny[sgemm::kE4m3SkinnyCount] = {
     {256, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<4, 4, true>)},
 };
 
-// How an 8-bit block runs: the fused kernel that the plain product of twice the
-// columns would take (as much work and as many workgroups), or two products
-// whose K is split over workgroups, where the output has too few tiles.
-struct E4m3GatedPlan {
-    sgemm::E4m3Plan p;
-    bool products;
-    long long workspace_bytes;
-};
-
-E4m3GatedPlan e4m3_gated_plan(int M, int N, int K, int cus, bool aligned, long long ws)
+// An 8-bit block takes the kernel that the plain product of twice the columns
+// would take: as much work, as many workgroups and, with a K split, as many
+// partial sums.  But up to 16 rows always stream: the gated form reads its rows of A
+// once for both weights, which the plain one's rates do not know (8192 x 8192,
+// microseconds: 1 row 25.7, against 37.2 with K split over tiles; 11 rows 27.0
+// against 29.5).
+sgemm::E4m3Plan e4m3_gated_plan(int M, int N, int K, int cus, bool aligned, long long ws)
 {
+    if (M <= sgemm::kE4m3Skinny[0].rows) return {-1, 1, K, 0, 0.0};
     const int wide = N <= sgemm::kMaxDim / 2 ? 2 * N : sgemm::kMaxDim;
-    E4m3GatedPlan best = {sgemm::e4m3_plan(M, wide, K, cus, aligned, 0), false, 0};
-    if (M <= sgemm::kE4m3Skinny[0].rows) return best;
-    const sgemm::E4m3Plan two = sgemm::e4m3_plan(M, N, K, cus, aligned, ws / 2);
-    const double ns = 2.0 * two.ns + kGateReduceNs;
-    if (two.kernel >= 0 && two.kernel < sgemm::kE4m3TileCount && two.splits > 1 &&
-        (best.p.kernel == sgemm::kE4m3None || ns < best.p.ns))
-        best = {two, true, gate_parts_bytes(M, N, two.splits)};
-    return best;
+    sgemm::E4m3Plan p = sgemm::e4m3_plan(M, wide, K, cus, aligned, ws);
+    if (p.splits > 1) p.workspace_bytes = gate_parts_bytes(M, N, p.splits);
+    // (the halves' rows are padded one by one)
+    return p.workspace_bytes <= ws ? p : sgemm::e4m3_plan(M, wide, K, cus, aligned, 0);
 }
 
 hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const float *scale_a, const void *Bg, int ldg,
@@ -609,9 +607,9 @@ hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const flo
     hipError_t err = device_cus(&cus);
     if (err != hipSuccess) return err;
     const bool aligned = e4m3_aligned(A, lda, Bg, ldg) && e4m3_aligned(A, lda, Bu, ldu);
-    const E4m3GatedPlan plan =
+    const sgemm::E4m3Plan plan =
         e4m3_gated_plan(M, N, K, cus, aligned, ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)ws_bytes);
-    if (plan.p.kernel == sgemm::kE4m3None) return hipErrorInvalidValue;
+    if (plan.kernel == sgemm::kE4m3None) return hipErrorInvalidValue;
     sgemm::E4m3GatedArgs g = {};
     g.A = static_cast<const float *>(A);
     g.B = static_cast<const float *>(Bg);
@@ -624,42 +622,39 @@ hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const flo
     g.N = N;
     g.K = K;
     g.ldc = ldc;
-    g.k_chunk = plan.p.k_chunk;
-    g.splits = plan.p.splits;
+    g.k_chunk = plan.k_chunk;
+    g.splits = plan.splits;
     g.group_m = sgemm::kDefaultGroupM;
     g.xcd_remap = sgemm::kDefaultXcdRemap;
     g.alpha = 1.0f;
     g.gate = e;
-    if (plan.p.kernel < 0) {
-        const E4m3SkinnyKernel &s = kE4m3GatedSkinny[-1 - plan.p.kernel];
+    if (plan.kernel < 0) {
+        const E4m3SkinnyKernel &s = kE4m3GatedSkinny[-1 - plan.kernel];
         const long long wgs = sgemm::ceil_div_ll(N, 16), cap = max_wgs_per_launch(s.threads);
         return launch1(s.fn, dim3((unsigned)(wgs < cap ? wgs : cap)), s.threads, &g, stream);
     }
-    const sgemm::E4m3Tile &t = sgemm::kE4m3Tiles[plan.p.kernel];
-    const E4m3TileKernel &v = (plan.products ? kE4m3TileKernels : kE4m3GatedTiles)[plan.p.kernel];
+    const sgemm::E4m3Tile &t = sgemm::kE4m3Tiles[plan.kernel];
+    const E4m3TileKernel &v = kE4m3GatedTiles[plan.kernel];
     g.tiles_m = (int)sgemm::ceil_div_ll(M, t.bm);
-    g.tiles_n = (int)sgemm::ceil_div_ll(N, plan.products ? t.bn : t.bn / 2);
-    const int ldp = (int)sgemm::partial_ld(N);
-    for (int half = 0; half < (plan.products ? 2 : 1); ++half) {
-        if (plan.products) {
-            g.B = static_cast<const float *>(half ? Bu : Bg);
-            g.ld_b = half ? ldu : ldg;
-            g.ldc = ldp;
-            g.split_c = (long long)M * ldp;
-            g.C = static_cast<float *>(ws) + half * plan.p.splits * g.split_c;
-        }
-        const long long grid = (long long)g.tiles_m * g.tiles_n * g.splits, per = max_wgs_per_launch(v.threads);
-        if (grid > INT_MAX) return hipErrorInvalidValue;
-        for (long long base = 0; base < grid; base += per) {
-            g.wg_base = (int)base;
-            // (the plain kernels take the E4m3Args that g begins with)
-            err = launch1(aligned ? v.direct : v.reg, dim3((unsigned)(grid - base < per ? grid - base : per)),
-                          v.threads, &g, stream);
-            if (err != hipSuccess) return err;
-        }
+    g.tiles_n = (int)sgemm::ceil_div_ll(N, t.bn / 2);
+    if (plan.splits > 1) {
+        const int ldp = (int)sgemm::partial_ld(N);
+        g.split_c = (long long)M * ldp;
+        g.gate = sgemm::Gate{};
+        g.gate.pre_gate = static_cast<float *>(ws);
+        g.gate.pre_up = g.gate.pre_gate + plan.splits * g.split_c;
+        g.gate.ld_pre_gate = g.gate.ld_pre_up = ldp;
+        g.C = nullptr;
     }
-    if (!plan.products) return hipSuccess;
-    return launch_gate_reduce(e, M, N, plan.p.splits, static_cast<const float *>(ws), C, ldc, stream);
+    const long long grid = (long long)g.tiles_m * g.tiles_n * plan.splits, per = max_wgs_per_launch(v.threads);
+    for (long long base = 0; base < grid; base += per) {
+        g.wg_base = (int)base;
+        err = launch1(aligned ? v.direct : v.reg, dim3((unsigned)(grid - base < per ? grid - base : per)), v.threads,
+                      &g, stream);
+        if (err != hipSuccess) return err;
+    }
+    if (plan.splits <= 1) return hipSuccess;
+    return launch_gate_reduce(e, M, N, plan.splits, static_cast<const float *>(ws), C, ldc, stream);
 }
 
 // ---- the elementwise gradient -------------------------------------------------------------------

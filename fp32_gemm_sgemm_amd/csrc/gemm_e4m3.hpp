@@ -49,7 +49,8 @@ struct E4m3Args : EpiGemmArgs {
 };
 
 // With GATED, the two products of a gated feed-forward block (gate.hpp): B is the
-// gate's operand, B_up the other one.
+// gate's operand, B_up the other one.  With a K split C is null and the gate's
+// pre_gate and pre_up are the partial sums, split_c elements a split.
 struct E4m3GatedArgs : E4m3Args {
     const unsigned char *B_up;
     int64_t ld_b_up;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typen
     const int kb = w.split * g.k_chunk;
     const unsigned char *A = reinterpret_cast<const unsigned char *>(g.A) + kb;
     const unsigned char *B = reinterpret_cast<const unsigned char *>(g.B) + kb;
-    g.C += w.split * g.split_c;
+    if constexpr (!GATED) g.C += w.split * g.split_c;
     const int M = g.M, N = g.N, K = min(g.K - kb, g.k_chunk);
     constexpr int BC = GATED ? BN / 2 : BN;  // columns of C
     const int m0 = w.tm * BM, n0 = w.tn * BC;
@@ -267,7 +268,6 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typen
         }
         const auto ar = make_rsrc(reinterpret_cast<const float *>(A + k0), (int64_t)kOobOffset);
         const auto br = make_rsrc(reinterpret_cast<const float *>(B + k0), (int64_t)kOobOffset);
-        const auto br2 = make_rsrc(reinterpret_cast<const float *>((GATED ? B2 : B) + k0), (int64_t)kOobOffset);
 #pragma unroll
         for (int j = 0; j < A_LOADS; ++j) {
             const int off = (int)(FULL || a_col[j] < lim ? a_off[j] : kOobOffset);
@@ -278,8 +278,13 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typen
         for (int j = 0; j < B_LOADS; ++j) {
             const int off = (int)(FULL || b_col[j] < lim ? b_off[j] : kOobOffset);
             float *dst = smem + s * STAGE_FLOATS + A_FLOATS + (j * NW + wave) * 64 * 4;
-            if (GATED && b_up[j]) __builtin_amdgcn_raw_ptr_buffer_load_lds(br2, (lds_void *)dst, 16, off, 0, 0, 0);
-            else __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_void *)dst, 16, off, 0, 0, 0);
+            if constexpr (GATED) {
+                // (the operand chosen by its address: a branch here would cut the loop's schedule)
+                const auto bj = make_rsrc(reinterpret_cast<const float *>(b_base_of(j) + k0), (int64_t)kOobOffset);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(bj, (lds_void *)dst, 16, off, 0, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(br, (lds_void *)dst, 16, off, 0, 0, 0);
+            }
         }
     };
 
@@ -433,7 +438,12 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typen
         // a wave's share holds a block row of both sums: the plain form's bytes
         constexpr int H = NB / 2, WTC = WTN / 2;
         typedef float half_t __attribute__((ext_vector_type(H)));
-        const StagedGate<MB, WTC, RM, true> epi(g.gate, g.C, g.ldc, M, N, lane, n0 + wn * WTC);
+        Gate gate = g.gate;
+        if (g.splits > 1) {
+            gate.pre_gate += w.split * g.split_c;
+            gate.pre_up += w.split * g.split_c;
+        }
+        const StagedGate<MB, WTC, RM, true> epi(gate, g.C, g.ldc, M, N, lane, n0 + wn * WTC);
         float scale[RM];
 #pragma unroll
         for (int i = 0; i < RM; ++i) scale[i] = epi.row_scale(m0 + wm * WTM + i);

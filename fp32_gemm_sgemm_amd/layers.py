@@ -8,10 +8,26 @@ call (not necessarily the current one), work enqueued on `stream` or on torch's
 current one, no synchronisation.
 """
 import ctypes
+import functools
 
-from .binding import GATED_AUTO, SgemmGate, SgemmTensor, _check, load, sgemm_f32_workspace_size
+from .binding import GATED_AUTO, SgemmGate, SgemmTensor, _check, load
 from .ops import (_MAX_DIM, _activation, _elsewhere, _empty, _empty_codes, _gpu_of, _handle, _matrix, _norm_inputs,
                   _rows, _same_gpu, _scratch, _supplied, _torch, _vector)
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes_of(lib, name, index, *sizes):
+    """The workspace that an entry point wants for these sizes on GPU `index`
+    (the current one).  Kept: a call costs a microsecond, a tenth of a small one."""
+    nbytes = ctypes.c_size_t(0)
+    _check(getattr(lib, name)(*sizes, ctypes.byref(nbytes)), name)
+    return nbytes.value
+
+
+def _workspace(name, device, *sizes):
+    """(tensor or None, address, bytes) of that workspace."""
+    nbytes = _bytes_of(load(), name, device.index, *sizes)
+    return (*_scratch(nbytes, device), nbytes)
 
 
 # ---- the gated feed-forward block ------------------------------------------------------------
@@ -121,27 +137,30 @@ def gated_grad(grad, pre_gate, pre_up, activation="silu", *, out_gate=None, out_
         else:
             t = _empty((N,), device) if t is None else t
             sums.append((t, _vector(t, N, device, name)))
-    ws, ws_ptr, nbytes = None, None, ctypes.c_size_t(0)
-    if sums[0][0] is not None or sums[1][0] is not None:
-        _check(load().sgemm_f32_gated_grad_workspace(M, N, ctypes.byref(nbytes)), "sgemm_f32_gated_grad_workspace")
-        ws, ws_ptr = _scratch(nbytes.value, device)
-    code = load().sgemm_f32_gated_grad(
-        M, N, act, grad.data_ptr(), ldy, pre_gate.data_ptr(), ldg, pre_up.data_ptr(), ldu, outs[0][1], outs[0][2],
-        outs[1][1], outs[1][2], sums[0][1], sums[1][1], ws_ptr, nbytes.value, _handle(device))
-    del ws
-    _check(code, "sgemm_f32_gated_grad")
+    _gate_grad(M, N, act, grad, ldy, pre_gate, ldg, pre_up, ldu, *outs[0][1:], *outs[1][1:], sums[0][1], sums[1][1],
+               device)
     return outs[0][0], outs[1][0], sums[0][0], sums[1][0]
 
 
-def _products(batch, ta, tb, M, N, K, x, ldx, sx, y, ldy, sy, beta, out, ldo, so, workspace, device):
-    """out = op(X) op(Y) + beta * out over a batch, of checked operands' addresses."""
+def _gate_grad(M, N, act, grad, ldy, pre_gate, ldg, pre_up, ldu, dg, lddg, du, lddu, bias_gate, bias_up, device):
+    """The call with checked tensors and the outputs' addresses."""
+    ws, ws_ptr, nbytes = None, None, 0
+    if bias_gate is not None or bias_up is not None:
+        ws, ws_ptr, nbytes = _workspace("sgemm_f32_gated_grad_workspace", device, M, N)
+    code = load().sgemm_f32_gated_grad(M, N, act, grad.data_ptr(), ldy, pre_gate.data_ptr(), ldg, pre_up.data_ptr(),
+                                       ldu, dg, lddg, du, lddu, bias_gate, bias_up, ws_ptr, nbytes, _handle(device))
+    del ws
+    _check(code, "sgemm_f32_gated_grad")
+
+
+def _products(batch, ta, tb, M, N, K, x, ldx, sx, y, ldy, sy, out, ldo, so, workspace, device):
+    """out = op(X) op(Y) over a batch, of checked operands' addresses."""
     ws, ws_ptr, ws_bytes = None, None, 0
     if isinstance(workspace, _torch().Tensor):
         ws_ptr, ws_bytes = _supplied(workspace, device)
     elif workspace and M and N and K:
-        ws_bytes = sgemm_f32_workspace_size(ta, tb, M, N, K, ldx, ldy, ldo, batch)
-        ws, ws_ptr = _scratch(ws_bytes, device)
-    code = load().sgemm_f32_ex(ta, tb, M, N, K, 1.0, x, ldx, sx, y, ldy, sy, beta, out, ldo, so, batch, ws_ptr,
+        ws, ws_ptr, ws_bytes = _workspace("sgemm_f32_workspace_size", device, ta, tb, M, N, K, ldx, ldy, ldo, batch)
+    code = load().sgemm_f32_ex(ta, tb, M, N, K, 1.0, x, ldx, sx, y, ldy, sy, 0.0, out, ldo, so, batch, ws_ptr,
                                ws_bytes, _handle(device), None)
     del ws
     _check(code, "sgemm_f32_ex")
@@ -186,43 +205,45 @@ def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation=
     K2, N, ldg, ldu = _weights(B_gate, B_up, transb, device)
     if K2 != K:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    _matrix(grad, M, N, device, "grad")
-    tb = 1 if transb else 0
-    products = "A" in need or "B" in need
-    bias = None if "bias" in need else False
+    ldy = _matrix(grad, M, N, device, "grad")
+    ldpg, ldpu = _matrix(pre_gate, M, N, device, "pre_gate"), _matrix(pre_up, M, N, device, "pre_up")
+    act, tb = _activation(activation), 1 if transb else 0
+    torch = _torch()
     # one tensor of both weights: its products are single ones of twice the size
     merged = ldg == ldu and B_up.data_ptr() - B_gate.data_ptr() == 4 * N * (ldg if transb else 1) and \
         (transb or ldg >= 2 * N)
     # dG and dU side by side; halves that products read one by one start 16-byte aligned
     half = N if merged else (N + 3) & ~3
-    ld = max(2 * half + 3 & ~3, 4)
-    dz = _torch().empty_strided((M, 2 * half), (ld, 1), dtype=_torch().float32, device=device) if products else None
-    _, _, dbias_gate, dbias_up = gated_grad(
-        grad, pre_gate, pre_up, activation, out_gate=dz[:, :N] if products else False,
-        out_up=dz[:, half:half + N] if products else False, dbias_gate=bias, dbias_up=bias)
-    dA = dB_gate = dB_up = None
-    z, a = (dz.data_ptr() if products else 0), A.data_ptr()
+    ld = max((2 * half + 3) & ~3, 4)
+    dA = dB = dB_gate = dB_up = dbias_gate = dbias_up = dz = z = up = bias = None
+    if "A" in need or "B" in need:
+        dz = torch.empty_strided((M, 2 * half), (ld, 1), dtype=torch.float32, device=device)
+        z = dz.data_ptr()
+        up = z + 4 * half
+    if "bias" in need:
+        dbias_gate, dbias_up = _empty((N,), device), _empty((N,), device)
+        bias = dbias_gate.data_ptr(), dbias_up.data_ptr()
+    _gate_grad(M, N, act, grad, ldy, pre_gate, ldpg, pre_up, ldpu, z, ld, up, ld, *(bias or (None, None)), device)
+    a, k = A.data_ptr(), max(K, 1)
     if "A" in need:
         dA = _empty((M, K), device)
         if merged:
-            _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, B_gate.data_ptr(), ldg, 0, 0.0, dA.data_ptr(), max(K, 1), 0,
-                      workspace, device)
+            _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, B_gate.data_ptr(), ldg, 0, dA.data_ptr(), k, 0, workspace,
+                      device)
         else:
-            _pair(1 - tb, M, K, N, z, z + 4 * half, ld, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu, dA.data_ptr(),
-                  max(K, 1), workspace, device)
+            _pair(1 - tb, M, K, N, z, up, ld, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu, dA.data_ptr(), k, workspace,
+                  device)
     if "B" in need:
         if transb:
             dB = _empty((2, N, K), device)
-            _products(2, 1, 0, N, K, M, z, ld, half, a, lda, 0, 0.0, dB.data_ptr(), max(K, 1), N * K, workspace, device)
-            dB_gate, dB_up = dB[0], dB[1]
+            _products(2, 1, 0, N, K, M, z, ld, half, a, lda, 0, dB.data_ptr(), k, N * K, workspace, device)
         elif merged:
             dB = _empty((K, 2 * N), device)
-            _products(1, 1, 0, K, 2 * N, M, a, lda, 0, z, ld, 0, 0.0, dB.data_ptr(), max(2 * N, 1), 0, workspace, device)
-            dB_gate, dB_up = dB[:, :N], dB[:, N:]
+            _products(1, 1, 0, K, 2 * N, M, a, lda, 0, z, ld, 0, dB.data_ptr(), max(2 * N, 1), 0, workspace, device)
         else:
             dB = _empty((2, K, N), device)
-            _products(2, 1, 0, K, N, M, a, lda, 0, z, ld, half, 0.0, dB.data_ptr(), max(N, 1), K * N, workspace, device)
-            dB_gate, dB_up = dB[0], dB[1]
+            _products(2, 1, 0, K, N, M, a, lda, 0, z, ld, half, dB.data_ptr(), max(N, 1), K * N, workspace, device)
+        dB_gate, dB_up = (dB[:, :N], dB[:, N:]) if merged and not transb else (dB[0], dB[1])
     return dA, dB_gate, dB_up, dbias_gate, dbias_up
 
 
@@ -264,10 +285,7 @@ def gemm_e4m3_gated(A, scale_a, B_gate, scale_gate, B_up, scale_up, *, bias_gate
     if isinstance(workspace, torch.Tensor):
         ws_ptr, ws_bytes = _supplied(workspace, device)
     elif workspace:
-        nbytes = ctypes.c_size_t(0)
-        _check(load().sgemm_e4m3_gated_workspace(M, N, K, ctypes.byref(nbytes)), "sgemm_e4m3_gated_workspace")
-        ws_bytes = nbytes.value
-        ws, ws_ptr = _scratch(ws_bytes, device)
+        ws, ws_ptr, ws_bytes = _workspace("sgemm_e4m3_gated_workspace", device, M, N, K)
     code = load().sgemm_e4m3_gated(M, N, K, A.data_ptr(), lda, sa, B_gate.data_ptr(), ldg, sg, B_up.data_ptr(), ldu,
                                    su, out.data_ptr(), ldc, ctypes.byref(g), ws_ptr, ws_bytes, _handle(device))
     del ws
@@ -347,14 +365,12 @@ def layernorm_backward(grad, s, weight=None, *, eps=1e-5, dsum=None, out=None, n
         lddx = _matrix(out, rows, D, device, "out")
     dw = _empty((D,), device) if weight is not None and need_weight else None
     db = _empty((D,), device) if need_bias else None
-    ws, ws_ptr, nbytes = None, None, ctypes.c_size_t(0)
+    ws, ws_ptr, nbytes = None, None, 0
     if dw is not None or db is not None:
-        _check(load().sgemm_layernorm_f32_grad_workspace(rows, D, ctypes.byref(nbytes)),
-               "sgemm_layernorm_f32_grad_workspace")
-        ws, ws_ptr = _scratch(nbytes.value, device)
+        ws, ws_ptr, nbytes = _workspace("sgemm_layernorm_f32_grad_workspace", device, rows, D)
     code = load().sgemm_layernorm_f32_grad(
         rows, D, grad.data_ptr(), ldy, s.data_ptr(), lds, w, float(eps), g, ldds, out.data_ptr(), lddx,
-        dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None, ws_ptr, nbytes.value,
+        dw.data_ptr() if dw is not None else None, db.data_ptr() if db is not None else None, ws_ptr, nbytes,
         _handle(device))
     del ws
     _check(code, "sgemm_layernorm_f32_grad")
@@ -377,25 +393,34 @@ def _plane(t, name):
 
 def _tensor_list(tensors, out, device):
     """The C array of the tensors (and of what is written for each)."""
-    flat = []
+    flat, float32, index = [], _torch().float32, device.index
     for i, x in enumerate(tensors):
-        rows, cols, ldx = _plane(x, "a tensor")
-        _same_gpu(device, x, "a tensor")
+        # (the common case first: a list of many little tensors is a call's whole time)
+        if x.dtype is float32 and x.is_contiguous():
+            rows, cols, ldx = 1, x.numel(), 0
+        else:
+            rows, cols, ldx = _plane(x, "a tensor")
+        if x.get_device() != index:
+            _same_gpu(device, x, "a tensor")
         ptr = x.data_ptr()
-        y, ldy = ptr, ldx
-        if out is not None:
-            to = out[i]
-            if to.shape != x.shape:
-                raise ValueError(f"out must have the tensors' shapes: {tuple(to.shape)} for {tuple(x.shape)}")
+        if out is None:
+            flat += (ptr, ptr, rows, cols, ldx, ldx)
+            continue
+        to = out[i]
+        if to.shape != x.shape:
+            raise ValueError(f"out must have the tensors' shapes: {tuple(to.shape)} for {tuple(x.shape)}")
+        if to.get_device() != index:
             _same_gpu(device, to, "out")
-            y = to.data_ptr()
+        if to.dtype is float32 and to.is_contiguous():
+            orows, ocols, ldy = 1, cols if rows == 1 else to.numel(), 0
+        else:
             orows, ocols, ldy = _plane(to, "out")
-            if (orows, ocols) != (rows, cols):
-                # one of the two is a run and the other has gaps between its rows
-                rows, cols = x.shape
-                ldx, ldy = ldx or cols, ldy or cols
-        flat += (ptr, y, rows, cols, ldx, ldy)
-    return (SgemmTensor * len(tensors)).from_buffer((ctypes.c_longlong * max(len(flat), 1))(*flat)) if flat else None
+        if orows != rows or ocols != cols:
+            # one of the two is a run and the other has gaps between its rows
+            rows, cols = x.shape
+            ldx, ldy = ldx or cols, ldy or cols
+        flat += (ptr, to.data_ptr(), rows, cols, ldx, ldy)
+    return (SgemmTensor * len(tensors)).from_buffer((ctypes.c_longlong * len(flat))(*flat))
 
 
 def _many(tensors, out, device, call):
@@ -403,11 +428,9 @@ def _many(tensors, out, device, call):
     as a tensor without dimensions."""
     torch = _torch()
     array = _tensor_list(tensors, out, device)
-    nbytes = ctypes.c_size_t(0)
-    _check(load().sgemm_clip_f32_workspace(len(tensors), ctypes.byref(nbytes)), "sgemm_clip_f32_workspace")
-    ws, ws_ptr = _scratch(nbytes.value, device)
+    ws, ws_ptr, nbytes = _workspace("sgemm_clip_f32_workspace", device, len(tensors))
     norm = torch.empty((), dtype=torch.float32, device=device)
-    call(len(tensors), array, norm.data_ptr(), ws_ptr, nbytes.value)
+    call(len(tensors), array, norm.data_ptr(), ws_ptr, nbytes)
     del ws
     return norm
 

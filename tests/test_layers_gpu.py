@@ -470,6 +470,26 @@ def test_gated_special_values():
         ops_ref.within(y[rest], Y, ty, f"form {form}")
 
 
+@pytest.mark.parametrize("tb", [False, True])
+def test_gated_backward_of_unlike_strides(tb):
+    """Two weight tensors whose rows are not the same distance apart, and sizes at
+    which the two products of dA run together and one after the other; with a
+    workspace, a little one and none."""
+    for M, N, K, pad in ((70, 130, 96, 3), (40, 2000, 50, 0), (40, 2000, 50, 2), (600, 700, 600, 0)):
+        A, dy, G, U = normal(M, K, seed=1), normal(M, N, seed=2), normal(M, N, seed=3), normal(M, N, seed=4)
+        (Bg, _), (hg, _) = weights(N, K, tb, False, 0, 0, 5)
+        (_, Bu), (_, hu) = weights(N, K, tb, False, pad, 0, 5)
+        w = [v.astype(np.float64) for v in (dy, A, G, U)]
+        dA, dBg, dBu, ta, tg, tu = ref.gated_backward(w[0], w[1], hg, hu, w[2], w[3], "silu")
+        if tb:
+            dBg, dBu, tg, tu = dBg.T, dBu.T, tg.T, tu.T
+        for ws in (True, False, torch.empty(1 << 12, dtype=torch.uint8, device="cuda"),
+                   torch.empty(1 << 26, dtype=torch.uint8, device="cuda")):
+            got = sg.sgemm_gated_backward(dev(dy), dev(A), Bg, Bu, pre_gate=dev(G), pre_up=dev(U), transb=tb, workspace=ws)
+            for what, g, want, t in zip(("dA", "dB_gate", "dB_up"), got, (dA, dBg, dBu), (ta, tg, tu)):
+                ops_ref.within(f64(g), want, t, f"{what} {M}x{N}x{K}")
+
+
 GRAD_SHAPES = [(1, 1, 1), (1, 300, 65), (5, 3, 40), (70, 130, 96), (129, 257, 65), (300, 64, 100), (33, 1030, 20)]
 
 
