@@ -9,7 +9,9 @@ import tempfile
 import numpy as np
 import pytest
 
+import e4m3_cases
 import fp32_gemm_sgemm_amd as sg
+import layers_cases
 import layers_ref as ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -395,3 +397,25 @@ def test_reference_gated_gradient_is_the_derivative():
                 up, down = list(args), list(args)
                 up[k], down[k] = args[k] + e, args[k] - e
                 assert abs((f(*up) - f(*down)) / (2 * h) - want[i]) < 1e-6, (name, k, i)
+
+
+# ---- the sizes that stand for the gated 8-bit kernels ---------------------------------------------------------
+
+def test_gated_8_bit_cases_reach_their_kernels(tmp_path):
+    planner = e4m3_cases.Planner(str(tmp_path))
+    cases = layers_cases.E4M3_GATED
+    plans = planner.plans([(m, 2 * n, k, al, ws) for _, m, n, k, al, ws, _ in cases])
+    for case, (kernel, splits, _) in zip(cases, plans):
+        if case[1] > 16:
+            assert (kernel, splits) == (case[0], case[6]), case
+    for name, reg in planner.kernels():
+        for aligned in (True, False) if reg else (True,):
+            mine = [c for c in cases if c[0] == name and c[4] == aligned]
+            assert mine, (name, aligned)
+            if name in e4m3_cases.SKINNY:
+                assert all(c[1] <= int(name[4:]) for c in mine)
+                continue
+            ks = [c[3] for c in mine if c[6] == 1]
+            assert any(c[6] > 1 for c in mine) and any(k % 16 for k in ks), (name, aligned)
+            assert min(ks) <= e4m3_cases.SLICE[name], (name, aligned)
+            assert max(ks) > e4m3_cases.SLICE[name] * e4m3_cases.STAGES[name], (name, aligned)

@@ -8,9 +8,11 @@ import pytest
 import torch
 
 import fp32_gemm_sgemm_amd as sg
+import layers_cases
 import layers_ref as ref
 import ops_ref
 from gpu_cases import note, place
+from test_e4m3_kernels_gpu import codes as half_codes
 
 pytestmark = pytest.mark.gpu
 
@@ -639,6 +641,64 @@ def test_gemm_e4m3_gated(M, N, K, pad):
     Y, _, _, ty, _, _ = ref.gated(A / f64(sa)[:, None], Bg.T / f64(sb), Bu.T, K + 3, None, None, name)
     y = sg.gemm_e4m3_gated(a, None, b, None, c, sc, activation=name)
     ops_ref.within(f64(y), Y, ty, "no scales")
+
+
+@pytest.mark.parametrize("case", layers_cases.E4M3_GATED, ids=lambda c: f"{c[0]}-{c[1]}x{c[2]}x{c[3]}-" +
+                         ("aligned" if c[4] else "any") + ("-split" if c[6] > 1 else ""))
+def test_each_gated_e4m3_kernel(case):
+    """Each kernel with every part of its epilogue against 64 bits, and the same
+    bits from the build that sets LDS to NaN before each refill.  The codes are
+    multiples of 1/2 up to 8: products are multiples of 1/4 up to 64, so up to
+    2^16 of them add to an exact float32 in any order, and only the epilogue's
+    roundings are left."""
+    _, M, N, K, aligned, workspace, _ = case
+    note(f"gated e4m3 {case}")
+    assert torch.cuda.get_device_properties(0).multi_processor_count == 256
+    i = layers_cases.E4M3_GATED.index(case)
+    gen = torch.Generator(device="cuda").manual_seed(i)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=gen, device="cuda")
+    # rows that are not aligned: those of A, of the gate's weights or of the other half's, by stride or start
+    off = None if aligned else i % 3
+    a, bg, bu = (half_codes(r, K, off != j, 3 if off == j and i % 2 else 0, gen) for j, r in enumerate((M, N, N)))
+    sa, sg_, su = torch.exp(rand(M)), torch.exp(rand(N)) / (10 * K ** 0.5), torch.exp(rand(N)) / (10 * K ** 0.5)
+    bias_g, bias_u = rand(N), rand(N)
+    out, ok = guarded(M, N)
+    pg, ok_g = guarded(M, N, pad=2)
+    pu, ok_u = guarded(M, N, pad=1)
+
+    def call():
+        sg.gemm_e4m3_gated(a, sa, bg, sg_, bu, su, bias_gate=bias_g, bias_up=bias_u, activation="silu", pre_gate=pg,
+                           pre_up=pu, out=out, workspace=workspace)
+
+    def half(b, scale, bias):
+        s = torch.mm(a.float().double(), b.float().double().T.contiguous()).mul_(sa.double()[:, None]).mul_(scale.double())
+        t = s.abs() * (2 * ops_ref.U)  # two scale factors
+        s += bias.double()
+        return s, t.add_(s.abs() * ops_ref.U).add_(1e-37)
+
+    def near(got, want, bound, what):
+        off = (got.double() - want).abs_() > bound
+        assert not bool((off | torch.isnan(got)).any()), (what, int(off.sum()), torch.nonzero(off)[:1].tolist())
+    call()
+    torch.cuda.synchronize()
+    ok(), ok_g(), ok_u()
+    g, tg = half(bg, sg_, bias_g)
+    near(pg, g, tg, "pre_gate")
+    act = g * torch.sigmoid(g)
+    ta = tg.mul_(ops_ref.LIPSCHITZ).add_(g.abs_() * ops_ref.ACT_ERR)
+    del g
+    u, tu = half(bu, su, bias_u)
+    near(pu, u, tu, "pre_up")
+    # (ta tu: both factors off at once)
+    y, ty = act * u, ta * u.abs() + act.abs() * tu + ta * tu
+    near(out, y, ty + ops_ref.U * y.abs() + 1e-37, "out")
+    del act, ta, u, tu, y, ty
+    held = out.clone(), pg.clone(), pu.clone()
+    with sg.library(sg.POISON_LIB_PATH):
+        call()
+        assert all(torch.equal(x, y) for x, y in zip((out, pg, pu), held)), "race check"
 
 
 def test_gemm_e4m3_gated_nan_codes():
