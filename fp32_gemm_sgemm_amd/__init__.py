@@ -5,8 +5,10 @@ C = alpha * op(A) x op(B) + beta * C with optional transposed operands, strided
 batches and K split across workgroups.  This package holds its thin ctypes
 binding (binding.py) with the operators around a product (ops.py: bias,
 activation and residual in the epilogue with their gradients, RMS norms, 8-bit
-quantisation and products), the seeded input generators (inputs.py) and host-side
-counting (metrics.py).  libsgemm_lds_poison.so is the same code built as an
+quantisation and products), what else a model's layer and its training step
+need (layers.py: gated feed-forward blocks, layer norms, their gradients, and
+gradients clipped to a norm), the seeded input generators (inputs.py) and
+host-side counting (metrics.py).  libsgemm_lds_poison.so is the same code built as an
 LDS race check, for the tests; libsgemm_timeline.so is the same code with
 clock readings inside the direct-load kernel, which timeline.py reports.  The
 library is loaded on first use; if it is missing, every entry point raises.

@@ -18,6 +18,11 @@
 // float64 at float32's rate.)  The mean is kept in two float32 parts, so that a
 // row whose mean is far from zero loses nothing but its own representation.
 //
+// Measured (microseconds, TB/s of what has to be read and written): 8192 x 8192 98 and
+// 5.5, with the residual and S stored 200 and 5.4, its codes 180 and 4.9 (float64 work
+// for two values of Y an element beside the loads), the gradient with dS 202 and 5.3;
+// 65536 x 512 42, 100, 85 and 101.
+//
 // A code is that of Y / scale in float64, rounded to float32 and then to 8 bits,
 // so that next to the border of two codes it goes the formula's way but for the
 // rounding of S.  It needs a second reduction, as the largest |Y| is not a

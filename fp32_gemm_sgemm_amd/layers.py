@@ -467,8 +467,9 @@ def clip_grad_norm(tensors, max_norm, *, eps=1e-6, out=None, stream=None):
     that of all their elements, which is returned (on the GPU, as grad_norm()).
 
     The tensors are scaled in place, or `out`, a list of tensors of the same
-    shapes, receives the scaled ones and they are left as they are.  Nothing
-    waits for the GPU, so a norm that is not finite is the caller's to look at.
+    shapes, receives the scaled ones and they are left as they are.  No two may
+    share memory (name a shared tensor once).  Nothing waits for the GPU, so a
+    norm that is not finite is the caller's to look at.
     """
     tensors = list(tensors)
     device = _list_device(tensors)

@@ -222,7 +222,7 @@ typedef struct sgemm_tensor {
  * Squares and sums are float64, and the factor is taken from the unrounded n
  * and rounded once.  A NaN, or an infinity, anywhere makes n so: the factor is
  * then NaN, or 0.  Where every y is its x and the factor is 1 nothing is
- * written.  Fewer than 96 tensors take two launches, or one if they are small; more take
+ * written.  Up to 96 tensors take two launches, or one if they are small; more take
  * one for every 96 besides.
  */
 int sgemm_clip_f32(int count, const sgemm_tensor *tensors, float max_norm, float eps, float *norm,
