@@ -230,16 +230,15 @@ template <bool HERE, bool WRITE> __global__ void __launch_bounds__(kClipThreads)
                                  clip_factor(a, total[0]));
 }
 
-// All of it by one workgroup.
-template <bool HERE, bool WRITE> __global__ void __launch_bounds__(kClipOneThreads) clip_one_kernel(ClipArgs a)
+// All of it by one workgroup.  (So few chunks are few tensors: the table is `here`.)
+template <bool WRITE> __global__ void __launch_bounds__(kClipOneThreads) clip_one_kernel(ClipArgs a)
 {
     __shared__ RowSums<kClipOneThreads> sums;
-    const ClipTensor *const table = HERE ? a.here : a.table;
-    double total[1] = {clip_squares<kClipOneThreads>(a, table, 0, 1)};
+    double total[1] = {clip_squares<kClipOneThreads>(a, a.here, 0, 1)};
     int turn = 0;
     row_all<kClipOneThreads, AddOp>(total, &sums, turn);
     if (threadIdx.x == 0 && a.norm) *a.norm = (float)sqrt(total[0]);
-    if constexpr (WRITE) clip_write<kClipOneThreads>(a, table, 0, 1, clip_factor(a, total[0]));
+    if constexpr (WRITE) clip_write<kClipOneThreads>(a, a.here, 0, 1, clip_factor(a, total[0]));
 }
 
 // A part of a table that is too long for a launch, to the workspace.

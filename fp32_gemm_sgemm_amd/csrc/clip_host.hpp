@@ -4,19 +4,21 @@
 // Chunks that one workgroup does alone in one launch (16384 elements).  Above,
 // two launches are quicker.
 constexpr int kClipOneChunks = 4;
+static_assert(kClipOneChunks <= sgemm::kClipInline, "their table travels with the launch");
 
 struct ClipKernels {
-    const void *norm, *scale, *one;
+    const void *norm, *scale;
 };
 template <bool HERE, bool WRITE> ClipKernels clip_kernels()
 {
     return {reinterpret_cast<const void *>(&sgemm::clip_norm_kernel<HERE>),
-            reinterpret_cast<const void *>(&sgemm::clip_scale_kernel<HERE, WRITE>),
-            reinterpret_cast<const void *>(&sgemm::clip_one_kernel<HERE, WRITE>)};
+            reinterpret_cast<const void *>(&sgemm::clip_scale_kernel<HERE, WRITE>)};
 }
 // by where the table is (the launch's arguments, memory) and whether y is written
 const ClipKernels kClipKernels[2][2] = {{clip_kernels<true, false>(), clip_kernels<true, true>()},
                                         {clip_kernels<false, false>(), clip_kernels<false, true>()}};
+const void *const kClipOne[2] = {reinterpret_cast<const void *>(&sgemm::clip_one_kernel<false>),
+                                 reinterpret_cast<const void *>(&sgemm::clip_one_kernel<true>)};
 
 size_t clip_table_bytes(int count)
 {
@@ -155,8 +157,8 @@ hipError_t run_clip(bool write, int count, const sgemm_tensor *tensors, float ma
             for (int i = 0; i < n; ++i) a.here[i] = table[(size_t)i];
         }
         a.count = n;
+        if (chunks <= kClipOneChunks) return launch1(kClipOne[write ? 1 : 0], dim3(1), sgemm::kClipOneThreads, &a, stream);
         const ClipKernels &k = kClipKernels[a.table ? 1 : 0][write ? 1 : 0];
-        if (chunks <= kClipOneChunks) return launch1(k.one, dim3(1), sgemm::kClipOneThreads, &a, stream);
         a.parts = chunks < sgemm::kClipMaxWgs ? (int)chunks : sgemm::kClipMaxWgs;
         const hipError_t e = launch1(k.norm, dim3((unsigned)a.parts), sgemm::kClipThreads, &a, stream);
         if (e != hipSuccess) return e;

@@ -431,6 +431,40 @@ def test_gated_every_form(form, tb):
 
 
 @pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 9])
+def test_gated_few_rows(M, tb):
+    """Each kernel for few rows: with and without K split over a workgroup's waves (K up from 1024, fewer than 8192
+    columns), K staged once and several times, lengths that are no multiple of four, columns that a wave does not
+    fill; the same bits from the build that sets LDS to NaN before each refill."""
+    for N, K, pad in ((1, 1024, 0), (67, 1027, 1), (33, 1021, 0), (130, 4097, 3), (300, 9001, 0), (8195, 1026, 0), (515, 3, 1)):
+        name = ops_ref.ACTS[(M + N) % 5]
+        note(f"few rows {M}x{N}x{K} tb={tb} pad {pad}")
+        A = normal(M, K, seed=1)
+        (Bg, Bu), (hg, hu) = weights(N, K, tb, bool(N % 2), pad, 0, 2)
+        bg, bu = normal(N, seed=5), normal(N, seed=6)
+        Y, G, U, ty, tg, tu = ref.gated(A.astype(np.float64), hg, hu, K, bg.astype(np.float64), bu.astype(np.float64), name)
+        a, b, c = dev(A, pad), dev(bg), dev(bu)
+        out, ok = guarded(M, N)
+        pg, ok_g = guarded(M, N, pad=5)
+        pu, ok_u = guarded(M, N, pad=1)
+
+        def call():
+            sg.sgemm_gated(a, Bg, Bu, bias_gate=b, bias_up=c, activation=name, pre_gate=pg, pre_up=pu, out=out, transb=tb,
+                           form=sg.GATED_ROWS)
+            torch.cuda.synchronize()
+        call()
+        ops_ref.within(f64(pg), G, tg, "pre_gate")
+        ops_ref.within(f64(pu), U, tu, "pre_up")
+        ops_ref.within(f64(out), Y, ty, "out")
+        for check in (ok, ok_g, ok_u):
+            check()
+        held = out.clone(), pg.clone(), pu.clone()
+        with sg.library(sg.POISON_LIB_PATH):
+            call()
+        assert all(torch.equal(x, y) for x, y in zip((out, pg, pu), held)), "race check"
+
+
+@pytest.mark.parametrize("tb", [False, True])
 def test_gated_weights_of_unlike_strides(tb):
     """The two weights' rows are not the same distance apart; more workspace and
     none."""
