@@ -429,7 +429,7 @@ def _many(tensors, out, device, call):
     torch = _torch()
     array = _tensor_list(tensors, out, device)
     ws, ws_ptr, nbytes = _workspace("sgemm_clip_f32_workspace", device, len(tensors))
-    norm = torch.empty((), dtype=torch.float32, device=device)
+    norm = torch.empty_strided((), (), dtype=torch.float32, device=device)
     call(len(tensors), array, norm.data_ptr(), ws_ptr, nbytes)
     del ws
     return norm

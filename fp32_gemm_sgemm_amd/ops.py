@@ -39,7 +39,8 @@ def _elsewhere(device, stream):
             raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
         if stream != torch.cuda.current_stream(device):
             return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    # (the tensors are on a GPU, so torch has set it up: current_device() would look again)
+    if torch._C._cuda_getDevice() != device.index:
         return torch.cuda.device(device)
     return None
 
@@ -100,9 +101,9 @@ def _matrix(t, rows, cols, device, name):
 def _vector(t, n, device, name):
     if t.dtype != _torch().float32:
         raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     _same_gpu(device, t, name)
     return t.data_ptr()
@@ -110,6 +111,11 @@ def _vector(t, n, device, name):
 
 def _empty(shape, device):
     torch = _torch()
+    # (empty() takes a third longer, 0.4 us of a small call's 8 to 16)
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (max(shape[1], 1), 1), dtype=torch.float32, device=device)
+    if len(shape) == 1:
+        return torch.empty_strided(shape, (1,), dtype=torch.float32, device=device)
     return torch.empty(shape, dtype=torch.float32, device=device)
 
 
@@ -127,7 +133,7 @@ def _scratch(nbytes, device):
     if nbytes <= 0:
         return None, None
     torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     return ws, ws.data_ptr()
 
 
