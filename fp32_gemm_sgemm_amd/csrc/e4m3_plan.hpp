@@ -2,6 +2,8 @@
 // no HIP calls, so it can be exercised without a device.
 #pragma once
 
+#include <algorithm>
+
 #include "select.hpp"
 
 namespace sgemm {
@@ -62,7 +64,38 @@ struct E4m3Plan {
     double ns;  // its cost by the model
 };
 
-inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws)
+// What a gated block's plan counts besides, from memory that no cache holds.  With
+// few rows every workgroup waits for the same slices of the weights at about the
+// same time: a slice takes a tile's cold_ns at least, whoever else computes on the
+// compute unit meanwhile (`resident` workgroups share one), and all of them the
+// stream's time.  The streaming kernels read both weights' rows side by side, so half
+// the workgroups share the chip.  Measured, microseconds, launches included:
+//                         17 rows                     64                    128
+//   two of 8192 x 8192    64x128, K in 4   33.4       35.6                  56.2
+//                         64x128, K in 2   41.5       43.0                  49.0
+//                         64x128           59.5       60.8                  60.4
+//                         streamed         36.1       58.4
+//   two of 8192 x 2048    64x64            14.3       15.8                  17.4
+//                         64x64, K in 2    14.7       16.2                  23.3
+//                         streamed         13.2       24.8
+//   two of 2048 x 8192    64x64, K in 8    16.4       17.7                  24.0
+//                         64x128, K in 4   20.6       20.9                  22.2
+//                         streamed         17.1       28.6
+struct E4m3Cold {
+    int slice, resident;
+    double cold_ns;
+};
+constexpr E4m3Cold kE4m3Cold[kE4m3TileCount] = {{64, 1, 0.0}, {128, 2, 950.0}, {128, 3, 900.0}, {128, 5, 880.0}};
+constexpr int kE4m3ColdRows = 512;
+constexpr double kE4m3ColdBytesPerNs = 6000.0;
+// The streaming kernels of a gated block (in the order of kE4m3Skinny, up to 16 rows aside):
+// fill_ns, per 1024 codes of K the time of a workgroup, and the stream's rate, both by the rows.
+constexpr double kE4m3GatedFillNs[kE4m3SkinnyCount] = {0.0, 5500.0, 8500.0};
+constexpr double kE4m3GatedWgNs = 700.0, kE4m3GatedRowNs = 22.0;
+constexpr double kE4m3GatedBytesPerNs = 5000.0, kE4m3GatedBytesPerNsRow = 33.0;
+
+// gated: N counts the columns of both weights.
+inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws, bool gated = false)
 {
     E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0, 0.0};
     double best_t = -1.0;
@@ -74,6 +107,10 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
                      stream = (double)N * K / kE4m3StreamBytesPerNs;
         best = {-1 - i, 1, K > 0 ? K : 1, 0, 0.0};
         best_t = s.fill_ns + (work > stream ? work : stream);
+        if (gated)
+            best_t = kE4m3GatedFillNs[i] +
+                     std::max((double)K / 1024.0 * (kE4m3GatedWgNs + kE4m3GatedRowNs * M),
+                              (double)N * K / (kE4m3GatedBytesPerNs - kE4m3GatedBytesPerNsRow * M));
         break;
     }
     for (int i = 0; i < kE4m3TileCount; ++i) {
@@ -92,6 +129,14 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
             const double k = (double)(splits > 1 ? per : K) / 1024.0 * (aligned ? 1.0 : kE4m3RegCost);
             double t = v.fill_ns + k * (v.lat_ns + per_cu * v.rate_ns) +
                        4.0 * splits * (double)M * (double)N / kE4m3StoreBytesPerNs;
+            if (gated && M <= kE4m3ColdRows) {
+                const E4m3Cold &c = kE4m3Cold[i];
+                const double slices = k * 1024.0 / c.slice;
+                const double rounds = (double)ceil_div_ll((long long)per_cu, c.resident);
+                const double work = v.fill_ns + std::max(slices * rounds * c.cold_ns, (double)N * K / kE4m3ColdBytesPerNs) +
+                                    4.0 * splits * (double)M * (double)N / kE4m3StoreBytesPerNs;
+                t = t > work ? t : work;
+            }
             if (splits > 1)
                 t += kE4m3ReduceNs + 4.0 * (splits + 1) * (double)M * (double)N / kReduceBytesPerNs;
             if (best_t < 0.0 || t < best_t) {
@@ -102,6 +147,22 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
     }
     best.ns = best_t;
     return best;
+}
+
+// A gated block of N columns a weight takes the kernel of a product of twice the
+// columns: as much work, as many workgroups and, with a K split, as many partial
+// sums.  But up to 16 rows always stream: the gated form reads its rows of A once
+// for both weights, which the plain one's rates do not know (8192 x 8192,
+// microseconds: 1 row 25.7, against 37.2 with K split over tiles; 11 rows 27.0
+// against 29.5).
+inline E4m3Plan e4m3_gated_plan(int M, int N, int K, int cus, bool aligned, long long ws)
+{
+    if (M <= kE4m3Skinny[0].rows) return {-1, 1, K, 0, 0.0};
+    const int wide = N <= kMaxDim / 2 ? 2 * N : kMaxDim;
+    E4m3Plan p = e4m3_plan(M, wide, K, cus, aligned, ws, true);
+    // (the halves' rows are padded one by one)
+    if (p.splits > 1) p.workspace_bytes = 8ll * p.splits * M * partial_ld(N);
+    return p.workspace_bytes <= ws ? p : e4m3_plan(M, wide, K, cus, aligned, 0, true);
 }
 
 }  // namespace sgemm

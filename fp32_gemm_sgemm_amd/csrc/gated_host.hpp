@@ -551,22 +551,6 @@ const E4m3SkinnyKernel kE4m3GatedSkinny[sgemm::kE4m3SkinnyCount] = {
     {256, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<4, 4, true>)},
 };
 
-// An 8-bit block takes the kernel that the plain product of twice the columns
-// would take: as much work, as many workgroups and, with a K split, as many
-// partial sums.  But up to 16 rows always stream: the gated form reads its rows of A
-// once for both weights, which the plain one's rates do not know (8192 x 8192,
-// microseconds: 1 row 25.7, against 37.2 with K split over tiles; 11 rows 27.0
-// against 29.5).
-sgemm::E4m3Plan e4m3_gated_plan(int M, int N, int K, int cus, bool aligned, long long ws)
-{
-    if (M <= sgemm::kE4m3Skinny[0].rows) return {-1, 1, K, 0, 0.0};
-    const int wide = N <= sgemm::kMaxDim / 2 ? 2 * N : sgemm::kMaxDim;
-    sgemm::E4m3Plan p = sgemm::e4m3_plan(M, wide, K, cus, aligned, ws);
-    if (p.splits > 1) p.workspace_bytes = gate_parts_bytes(M, N, p.splits);
-    // (the halves' rows are padded one by one)
-    return p.workspace_bytes <= ws ? p : sgemm::e4m3_plan(M, wide, K, cus, aligned, 0);
-}
-
 hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const float *scale_a, const void *Bg, int ldg,
                           const float *scale_gate, const void *Bu, int ldu, const float *scale_up, float *C, int ldc,
                           const sgemm_gate *gate, void *ws, size_t ws_bytes, hipStream_t stream)
@@ -608,7 +592,7 @@ hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const flo
     if (err != hipSuccess) return err;
     const bool aligned = e4m3_aligned(A, lda, Bg, ldg) && e4m3_aligned(A, lda, Bu, ldu);
     const sgemm::E4m3Plan plan =
-        e4m3_gated_plan(M, N, K, cus, aligned, ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)ws_bytes);
+        sgemm::e4m3_gated_plan(M, N, K, cus, aligned, ws_bytes > (size_t)LLONG_MAX ? LLONG_MAX : (long long)ws_bytes);
     if (plan.kernel == sgemm::kE4m3None) return hipErrorInvalidValue;
     sgemm::E4m3GatedArgs g = {};
     g.A = static_cast<const float *>(A);

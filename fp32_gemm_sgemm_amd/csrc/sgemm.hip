@@ -1077,7 +1077,7 @@ int sgemm_e4m3_gated_workspace(int M, int N, int K, size_t *bytes)
     int cus = 0;
     const hipError_t e = device_cus(&cus);
     if (e != hipSuccess) return e;
-    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)e4m3_gated_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
+    *bytes = M > 0 && N > 0 && K > 0 ? (size_t)sgemm::e4m3_gated_plan(M, N, K, cus, true, LLONG_MAX).workspace_bytes : 0;
     return hipSuccess;
 }
 
