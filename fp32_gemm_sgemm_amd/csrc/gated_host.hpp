@@ -545,6 +545,12 @@ const E4m3TileKernel kE4m3GatedTiles[sgemm::kE4m3TileCount] = {
     {256, e4m3_gated_fn<64, 128, 32, 2, 2, 2, 32>(), e4m3_gated_reg_fn<64, 128, 32, 2, 2, 32>()},
     {256, e4m3_gated_fn<64, 64, 32, 2, 2, 2, 16>(), e4m3_gated_reg_fn<64, 64, 32, 2, 2, 16>()},
 };
+// Up to 16 rows where 16 columns a workgroup leave compute units idle: 8 columns of each
+// weight (1 and 16 rows in a graph, microseconds, 16 and 8 columns: two weights of 1024 x
+// 4096 8.2 and 6.5, 10.0 and 8.1; 2048 x 8192 13.9 and 12.2, 15.9 and 13.3; with as many
+// workgroups as compute units, 4096 x 4096, 11.8 and 10.7, 12.0 and 13.0).
+const E4m3SkinnyKernel kE4m3GatedNarrow = {
+    128, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<2, 1, true, true>)};
 const E4m3SkinnyKernel kE4m3GatedSkinny[sgemm::kE4m3SkinnyCount] = {
     {128, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<2, 1, true>)},
     {256, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<4, 2, true>)},
@@ -613,8 +619,9 @@ hipError_t run_e4m3_gated(int M, int N, int K, const void *A, int lda, const flo
     g.alpha = 1.0f;
     g.gate = e;
     if (plan.kernel < 0) {
-        const E4m3SkinnyKernel &s = kE4m3GatedSkinny[-1 - plan.kernel];
-        const long long wgs = sgemm::ceil_div_ll(N, 16), cap = max_wgs_per_launch(s.threads);
+        const bool narrow = plan.kernel == -1 && sgemm::ceil_div_ll(N, 16) < cus;
+        const E4m3SkinnyKernel &s = narrow ? kE4m3GatedNarrow : kE4m3GatedSkinny[-1 - plan.kernel];
+        const long long wgs = sgemm::ceil_div_ll(N, narrow ? 8 : 16), cap = max_wgs_per_launch(s.threads);
         return launch1(s.fn, dim3((unsigned)(wgs < cap ? wgs : cap)), s.threads, &g, stream);
     }
     const sgemm::E4m3Tile &t = sgemm::kE4m3Tiles[plan.kernel];

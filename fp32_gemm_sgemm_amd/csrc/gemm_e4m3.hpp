@@ -517,19 +517,22 @@ __global__ void __launch_bounds__(WAVES_M * WAVES_N * 64) gemm_e4m3_kernel(typen
 // Rows of A past M and of B past N are read as the last
 // one and never stored; codes past K read as zero.
 // GATED: both products of a gated block, the rows of both weights streamed side
-// by side against the same codes of A.
-template <int W, int RM, bool GATED = false> struct SkinnyTraits {
+// by side against the same codes of A.  NARROW: 8 columns of each take the place of
+// 16, for twice the workgroups.
+template <int W, int RM, bool GATED = false, bool NARROW = false> struct SkinnyTraits {
     static constexpr int NT = W * 64;
     static constexpr int DEPTH = 3;
-    static constexpr int HALVES = GATED ? 2 : 1;
+    static constexpr int COLS = NARROW ? 8 : 16;
+    static constexpr int HALVES = GATED && !NARROW ? 2 : 1;
     static constexpr int LDS_FLOATS = W * HALVES * RM * 256;
 };
 
-template <int W, int RM, bool GATED = false>
+template <int W, int RM, bool GATED = false, bool NARROW = false>
 __global__ void __launch_bounds__(W * 64) gemm_e4m3_skinny_kernel(typename E4m3KernelArgs<GATED>::T g)
 {
-    typedef SkinnyTraits<W, RM, GATED> T;
-    constexpr int D = T::DEPTH, NH = T::HALVES;
+    static_assert(GATED || !NARROW, "two weights");
+    typedef SkinnyTraits<W, RM, GATED, NARROW> T;
+    constexpr int D = T::DEPTH, NH = T::HALVES, COLS = T::COLS;
     __shared__ __attribute__((aligned(16))) float red[T::LDS_FLOATS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -541,11 +544,15 @@ __global__ void __launch_bounds__(W * 64) gemm_e4m3_skinny_kernel(typename E4m3K
         __syncthreads();
     }
     // (64 bits: the last workgroup's next column can pass 2^31)
-    for (int64_t c0 = 16 * (int64_t)blockIdx.x; c0 < N; c0 += 16 * (int64_t)gridDim.x) {
+    for (int64_t c0 = COLS * (int64_t)blockIdx.x; c0 < N; c0 += COLS * (int64_t)gridDim.x) {
         const int n0 = (int)c0;
         const unsigned char *b[NH];
-        b[0] = reinterpret_cast<const unsigned char *>(g.B) + min(n0 + lr, N - 1) * g.ld_b;
-        if constexpr (GATED) b[1] = g.B_up + min(n0 + lr, N - 1) * g.ld_b_up;
+        b[0] = reinterpret_cast<const unsigned char *>(g.B) + min(n0 + lr % COLS, N - 1) * g.ld_b;
+        if constexpr (NARROW) {
+            if (lr >= COLS) b[0] = g.B_up + min(n0 + lr % COLS, N - 1) * g.ld_b_up;
+        } else if constexpr (GATED) {
+            b[1] = g.B_up + min(n0 + lr, N - 1) * g.ld_b_up;
+        }
         const unsigned char *a[RM];
 #pragma unroll
         for (int i = 0; i < RM; ++i)
@@ -636,10 +643,19 @@ __global__ void __launch_bounds__(W * 64) gemm_e4m3_skinny_kernel(typename E4m3K
                 for (int x = 1; x < W; ++x) s += red[(x * NH + half) * RM * 256 + o];
                 return s;
             };
-            v[0] = total(0);
-            if constexpr (GATED) u[0] = total(1);
             // accumulator r of lane l is D[4 (l / 16) + r][l mod 16]
             const int i = o >> 8, r = (o >> 6) & 3, l = o & 63;
+            if constexpr (NARROW) {
+                if ((l & 15) >= COLS) continue;
+            }
+            v[0] = total(0);
+            if constexpr (NARROW) {
+                u[0] = red[o + COLS];
+#pragma unroll
+                for (int x = 1; x < W; ++x) u[0] += red[x * RM * 256 + o + COLS];
+            } else if constexpr (GATED) {
+                u[0] = total(1);
+            }
             const int row = 16 * i + 4 * (l >> 4) + r, col = n0 + (l & 15);
             if (row < M && col < N) {
                 if constexpr (GATED) gate_apply<1>(g.gate, row, col, N, v, u);

@@ -42,6 +42,12 @@ E4M3_GATED = [
     ("64x64", 17, 1, 4000, False, True, 32),
     ("rows16", 1, 300, 4096, True, True, 1),
     ("rows16", 16, 101, 1037, False, True, 1),
+    # (from 4081 columns on a workgroup takes 16 of each weight instead of 8)
+    ("rows16", 9, 4080, 1037, False, True, 1),
+    ("rows16", 2, 4081, 600, True, True, 1),
+    ("rows16", 5, 8195, 1037, False, True, 1),
+    ("rows16", 16, 9, 300, True, True, 1),
+    ("rows16", 3, 7, 61, False, True, 1),
     ("rows32", 17, 515, 1050, True, False, 1),
     ("rows32", 31, 101, 1037, False, False, 1),
     ("rows64", 33, 515, 2002, True, False, 1),
