@@ -52,7 +52,7 @@ struct E4m3Args : EpiGemmArgs {
 // gate's operand, B_up the other one.  With a K split C is null and the gate's
 // pre_gate and pre_up are the partial sums, split_c elements a split.  Measured:
 // 4096 x 8192 x 8192 (two weights) 763 to 784 us, the rate of the plain 8192^3; one row
-// of 2048 x 512 4.3 us in the kernel, of 8192 x 8192 25.7 (5.2 TB/s), 64 rows of it 37.
+// of 2048 x 512 4.0 us in the kernel, of 8192 x 8192 25.7 (5.2 TB/s), 64 rows of it 37.
 struct E4m3GatedArgs : E4m3Args {
     const unsigned char *B_up;
     int64_t ld_b_up;
