@@ -104,8 +104,7 @@ def draw(rng):
     pad = rng.choice([0, 0, 1, 4, 16])  # elements between the end of a row and the next
     if kind == "clip":
         while True:
-            # (nine layers: with the norm 64 outputs, the most that a comparison takes)
-            case = {"kind": kind, "layers": _size(rng, 1, 9), "width": _size(rng, 16, 4096),
+            case = {"kind": kind, "layers": _size(rng, 1, 48), "width": _size(rng, 16, 4096),
                     "inner": _size(rng, 16, 8192), "max_norm": rng.choice([0.5, 1.0, 1e6]), "pad": pad}
             if _elements(case) <= MOST_ELEMENTS:
                 return case
