@@ -405,8 +405,12 @@ struct LnGradArgs {
     float eps;
 };
 
-//   g = dY w,  dX = r (g - mean(g)) - d r^3 mean(g d) + dS,
-//   dw = sum over rows of dY d r,  db = sum over rows of dY
+//   g = dY w,  h = d r,  dX = r (g - mean(g) - h mean(g h)) + dS,
+//   dw = sum over rows of dY h,  db = sum over rows of dY
+//
+// Both means are at most as large as g and h is at most sqrt(D), so nothing leaves
+// float32 whatever the row's size.  (As d r^3 mean(g d) the factor of d goes with the
+// inverse square of the spread: 0 in float32 from 1e23 on, infinite below 1e-19.)
 //
 // A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once)
 // and keeps the sums of its own columns in registers, as row_grad_kernel does;
@@ -440,11 +444,11 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
         const float *s = a.S + row * a.lds;
         const float *ds = a.dS ? a.dS + row * a.ldds : nullptr;
         float *dx = a.dX + row * a.lddx;
-        // r (g - mean g) - d c
-        auto write = [&](int col, const float (&g)[4], const float (&d)[4], float r, float mg, float c) {
+        // r (g - mean g - h mean(g h))
+        auto write = [&](int col, const float (&g)[4], const float (&h)[4], float r, float mg, float mgh) {
             float o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[j] = r * (g[j] - mg) - d[j] * c;
+            for (int j = 0; j < 4; ++j) o[j] = r * ((g[j] - mg) - h[j] * mgh);
             if (ds) {
                 float q[4];
                 load_cols<4>(ds + col, col, D, q);
@@ -490,20 +494,20 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
             const double e = q[0] * inv_d, rd = inv_sqrt(fmax(q[1] * inv_d - e * e, 0.0) + a.eps);
             const Mean m(x0 + e);
             const float r = (float)rd, mg = (float)(q[2] * inv_d);
-            const float c = (float)((q[3] - e * q[2]) * inv_d * rd * rd * rd);
+            const float mgh = (float)((q[3] - e * q[2]) * inv_d * rd);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int col = 4 * (i * NT + t);
                 if (col < D) {
-                    float g[4], d[4];
+                    float g[4], h[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         g[j] = y[i][j] * w[i][j];
-                        d[j] = m.from(x[i][j]);
-                        dw[i][j] += y[i][j] * (d[j] * r);
+                        h[j] = m.from(x[i][j]) * r;
+                        dw[i][j] += y[i][j] * h[j];
                         db[i][j] += y[i][j];
                     }
-                    write(col, g, d, r, mg, c);
+                    write(col, g, h, r, mg, mgh);
                 }
             }
         } else {
@@ -534,13 +538,13 @@ __global__ void __launch_bounds__(NT > 256 ? NT : 256) layernorm_grad_kernel(LnG
             const double e = q[0] * inv_d, rd = inv_sqrt(fmax(q[1] * inv_d - e * e, 0.0) + a.eps);
             const Mean m(x0 + e);
             const float r = (float)rd, mg = (float)(q[2] * inv_d);
-            const float c = (float)((q[3] - e * q[2]) * inv_d * rd * rd * rd);
+            const float mgh = (float)((q[3] - e * q[2]) * inv_d * rd);
             for (int64_t col = 4 * t; col < D; col += 4 * NT) {
                 float g[4], x[4];
                 load((int)col, g, x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = m.from(x[j]);
-                write((int)col, g, x, r, mg, c);
+                for (int j = 0; j < 4; ++j) x[j] = m.from(x[j]) * r;
+                write((int)col, g, x, r, mg, mgh);
             }
             if (a.rows3 && t == 0) a.rows3[row] = LnRow{m.hi, m.lo, r};
         }

@@ -1,0 +1,77 @@
+"""Operators of sgemm_layers.h at the ends of their ranges, against plain 64-bit
+implementations with the bounds of layers_bounds.py."""
+import numpy as np
+import pytest
+import torch
+
+import fp32_gemm_sgemm_amd as sg
+import layers_bounds as bounds
+import ops_ref
+from gpu_cases import note
+
+pytestmark = pytest.mark.gpu
+
+EPS = float(np.float32(1e-5))
+
+
+def normal(*shape, seed=0):
+    return np.random.default_rng(seed).standard_normal(shape).astype(np.float32)
+
+
+def dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to("cuda")
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy() if isinstance(t, torch.Tensor) else t.astype(np.float64)
+
+
+# ---- layer norm -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("stream", [False, True])
+@pytest.mark.parametrize("D", [5, 700, 1500, 3000, 6000, 9000, 17000])
+def test_layernorm_gradient_rows_of_every_size(D, stream):
+    """The gradient of the same rows, whose third term is (1/sigma^2) d times a
+    mean; then constant rows and rows that hold an infinity or NaN beside them."""
+    note(f"layernorm_backward {D} stream={stream}")
+    s = bounds.rows_of(D)
+    dy, w = normal(*s.shape, seed=1), normal(D, seed=2)
+    ds = normal(*s.shape, seed=3) if stream else None
+    S, DY, W, DS = dev(s), dev(dy), dev(w), dev(ds) if stream else None
+    dx, dw, db = sg.layernorm_backward(DY, S, W, dsum=DS)
+    X, DW, DB, tx, tw, tb = bounds.backward(f64(dy), f64(s), f64(w), EPS, f64(ds) if stream else None)
+    ops_ref.within(f64(dx), X, tx, "dx")
+    ops_ref.within(f64(dw), DW, tw, "dw")
+    ops_ref.within(f64(db), DB, tb, "db")
+    S[0] = 3.0
+    S[3, D // 2] = float("inf")
+    S[6, D - 1] = float("nan")
+    dx, _, _ = sg.layernorm_backward(DY, S, W, dsum=DS, need_weight=False, need_bias=False)
+    keep = [i for i in range(len(s)) if i not in (3, 6)]
+    X, _, _, tx, _, _ = bounds.backward(f64(dy)[keep], f64(S)[keep], f64(w), EPS, f64(ds)[keep] if stream else None)
+    ops_ref.within(f64(dx)[keep], X, tx, "dx beside rows that are not finite")
+    assert np.isnan(f64(dx)[[3, 6]]).all()
+
+
+def test_layernorm_gradient_of_many_rows_of_every_size():
+    """More than 512 rows of 4097 to 8192 values without sums have a form of their own."""
+    D = 5000
+    s, w = np.tile(bounds.rows_of(D), (60, 1)), normal(D, seed=2)
+    dy = normal(*s.shape, seed=1)
+    dx, dw, db = sg.layernorm_backward(dev(dy), dev(s), dev(w), need_weight=False, need_bias=False)
+    assert dw is None and db is None
+    X, _, _, tx, _, _ = bounds.backward(f64(dy), f64(s), f64(w), EPS)
+    ops_ref.within(f64(dx), X, tx)
+
+
+@pytest.mark.parametrize("D", [5, 700, 1500, 3000, 6000, 9000, 17000])
+def test_layernorm_gradient_of_small_rows_without_eps(D):
+    """r^3 of rows of 1e-20 and 1e-24 is past float32's range, r and dX are not."""
+    s = normal(4, D, seed=1) * np.float32([[1e-20], [1e-24], [1e-15], [1.0]])
+    dy, w = normal(4, D, seed=2), normal(D, seed=3)
+    dx, _, _ = sg.layernorm_backward(dev(dy), dev(s), dev(w), eps=0.0)
+    X, _, _, tx, _, _ = bounds.backward(f64(dy), f64(s), f64(w), 0.0)
+    ops_ref.within(f64(dx), X, tx)
+    s[1] = 7.0  # 0 / 0
+    dx, _, _ = sg.layernorm_backward(dev(dy), dev(s), dev(w), eps=0.0)
+    assert np.isnan(f64(dx)[1]).all() and np.isfinite(f64(dx)[[0, 2, 3]]).all()
