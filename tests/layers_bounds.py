@@ -120,3 +120,12 @@ def rows_of(D, seed=0):
     x[9] = 0
     x[9, 0] = -1e30
     return x
+
+
+def planted(D):
+    """(s, dy): rows whose sums, of s and s^2, of g and g h, need more than
+    float32: large values that cancel beside ones that count."""
+    big = 2.0 ** 26
+    s = np.tile([big, 1, 1, -big], D // 4).astype(np.float32)[None, :]
+    t = np.tile([-1, 1, 2, -1], D // 4).astype(np.float32)[None, :]
+    return s, t, np.tile([big, 1, 3, -big], D // 4).astype(np.float32)[None, :]

@@ -5,7 +5,7 @@ import pytest
 
 import layers_bounds as bounds
 import layers_ref
-from layers_bounds import rows_of
+from layers_bounds import planted, rows_of
 
 
 @pytest.mark.parametrize("D", [5, 700, 3000, 20003])
@@ -27,6 +27,18 @@ def test_kernel_arithmetic_is_within(D):
     dx, _, _, t, _, _ = bounds.backward(f(dy[:1]), f(small), f(w), 0.0)
     assert (np.abs(bounds.kernel_backward(dy[:1], small, w, 0.0) - dx) <= t).all()
     assert not np.isfinite(bounds.kernel_backward(dy[:1], small, w, 0.0, cube=True)).all()
+
+
+@pytest.mark.parametrize("D", [64, 700, 2052, 20004])
+def test_row_sums_in_float32_are_outside(D):
+    s, t, dy = planted(D)
+    f = lambda v: v.astype(np.float64)  # noqa: E731
+    y, ty = bounds.forward(f(s), None, None, 0.0)
+    assert (np.abs(bounds.kernel_forward(s, None, None, 0.0) - y) <= ty).all()
+    assert (np.abs(bounds.kernel_forward(s, None, None, 0.0, np.float32) - y) > ty).any()
+    dx, _, _, tx, _, _ = bounds.backward(f(dy), f(t), None, 0.0)
+    assert (np.abs(bounds.kernel_backward(dy, t, None, 0.0) - dx) <= tx).all()
+    assert (np.abs(bounds.kernel_backward(dy, t, None, 0.0, np.float32) - dx) > tx).any()
 
 
 def test_the_two_references_agree():

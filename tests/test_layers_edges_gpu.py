@@ -28,6 +28,15 @@ def f64(t):
 
 # ---- layer norm -----------------------------------------------------------------------------------
 
+@pytest.mark.parametrize("D", [5, 700, 1500, 3000, 6000, 9000, 17000])
+def test_layernorm_rows_of_every_size(D):
+    """Rows from 1e-3 to 1e36, far from zero, with one value of 1e30; every form."""
+    note(f"layernorm {D}")
+    s, w, b = bounds.rows_of(D), normal(D, seed=1), normal(D, seed=2)
+    y, _ = sg.layernorm(dev(s), dev(w), dev(b))
+    ops_ref.within(f64(y), *bounds.forward(f64(s), f64(w), f64(b), EPS))
+
+
 @pytest.mark.parametrize("stream", [False, True])
 @pytest.mark.parametrize("D", [5, 700, 1500, 3000, 6000, 9000, 17000])
 def test_layernorm_gradient_rows_of_every_size(D, stream):
@@ -75,3 +84,14 @@ def test_layernorm_gradient_of_small_rows_without_eps(D):
     s[1] = 7.0  # 0 / 0
     dx, _, _ = sg.layernorm_backward(dev(dy), dev(s), dev(w), eps=0.0)
     assert np.isnan(f64(dx)[1]).all() and np.isfinite(f64(dx)[[0, 2, 3]]).all()
+
+
+@pytest.mark.parametrize("D", [64, 700, 2052, 5000, 9000, 20004])
+def test_row_sums_are_float64(D):
+    """Large values that cancel beside ones that count, in a thread's own sums."""
+    s, t, dy = bounds.planted(D)
+    y, _ = sg.layernorm(dev(s), eps=0.0)
+    ops_ref.within(f64(y), *bounds.forward(f64(s), None, None, 0.0), "y")
+    dx, _, _ = sg.layernorm_backward(dev(dy), dev(t), eps=0.0)
+    X, _, _, tx, _, _ = bounds.backward(f64(dy), f64(t), None, 0.0)
+    ops_ref.within(f64(dx), X, tx, "dx")
