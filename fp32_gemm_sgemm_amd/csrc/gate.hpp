@@ -33,15 +33,18 @@ struct Gate {
 template <int W>
 __device__ __forceinline__ void gate_apply(const Gate &e, int row, int col, int N, float (&g)[W], float (&u)[W])
 {
-    auto affine = [&](const float *scale, const float *bias, float sa, float (&v)[W]) {
+    const float sa = e.scale_a ? load_global(e.scale_a + row) : 1.0f;
+    // (one scale after the other: their product may leave float32 where the sum's does not)
+    auto affine = [&](const float *scale, const float *bias, float (&v)[W]) {
         float x[W];
+        if (e.scale_a) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[j] *= sa;
+        }
         if (scale) {
             load_cols<W>(scale + col, col, N, x);
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[j] *= sa * x[j];
-        } else if (e.scale_a) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) v[j] *= sa;
+            for (int j = 0; j < W; ++j) v[j] *= x[j];
         }
         if (bias) {
             load_cols<W>(bias + col, col, N, x);
@@ -49,9 +52,8 @@ __device__ __forceinline__ void gate_apply(const Gate &e, int row, int col, int 
             for (int j = 0; j < W; ++j) v[j] += x[j];
         }
     };
-    const float sa = e.scale_a ? load_global(e.scale_a + row) : 1.0f;
-    affine(e.scale_gate, e.bias_gate, sa, g);
-    affine(e.scale_up, e.bias_up, sa, u);
+    affine(e.scale_gate, e.bias_gate, g);
+    affine(e.scale_up, e.bias_up, u);
     if (e.pre_gate) store_row<W>(e.pre_gate + row * e.ld_pre_gate + col, col, N, g, 1.0f, 0.0f);
     if (e.pre_up) store_row<W>(e.pre_up + row * e.ld_pre_up + col, col, N, u, 1.0f, 0.0f);
 #pragma unroll
@@ -126,8 +128,8 @@ template <int R, int WT, int RS, bool SCALES> struct StagedGate {
             const float *const p = lds + rr * WT + cc;
             f32x4 g = *reinterpret_cast<const f32x4 *>(p), u = *reinterpret_cast<const f32x4 *>(p + R * WT);
             if (SCALES) {
-                g *= sa * scale_gate;
-                u *= sa * scale_up;
+                g = g * sa * scale_gate;
+                u = u * sa * scale_up;
             }
             g += bias_gate;
             u += bias_up;

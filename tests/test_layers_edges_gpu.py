@@ -6,6 +6,7 @@ import torch
 
 import fp32_gemm_sgemm_amd as sg
 import layers_bounds as bounds
+import layers_cases
 import ops_ref
 from gpu_cases import note
 
@@ -95,3 +96,46 @@ def test_row_sums_are_float64(D):
     dx, _, _ = sg.layernorm_backward(dev(dy), dev(t), eps=0.0)
     X, _, _, tx, _, _ = bounds.backward(f64(dy), f64(t), None, 0.0)
     ops_ref.within(f64(dx), X, tx, "dx")
+
+
+# ---- the gated block of 8-bit operands ----------------------------------------------------------------
+
+# one size for each 8-bit kernel, whole and with K split, aligned and not
+E4M3_FORMS = list({(c[0], c[4], c[6] > 1, c[2] > 4080): c for c in layers_cases.E4M3_GATED}.values())
+
+
+@pytest.mark.parametrize("case", E4M3_FORMS, ids=lambda c: f"{c[0]}-{c[1]}x{c[2]}x{c[3]}-" +
+                         ("aligned" if c[4] else "any") + ("-split" if c[6] > 1 else ""))
+def test_scales_whose_product_leaves_float32(case):
+    """A row's scale and a column's act one after the other, as in the plain 8-bit
+    product: 2^-100 and 2^-52 on sums of 2^23 and more leave values that
+    float32 holds, 2^70 and 2^70 on a sum of zero leave zero."""
+    _, M, N, K, aligned, workspace, _ = case
+    note(f"gated e4m3 scales {case}")
+
+    def rows(n, value):
+        buf = torch.zeros(n, K if not aligned else -(-K // 16) * 16, dtype=torch.float8_e4m3fn, device="cuda")[:, :K]
+        return buf.copy_(value[:, None].to(torch.float8_e4m3fn)) if n else buf
+    m, n = torch.arange(M, device="cuda"), torch.arange(N, device="cuda")
+    empty = m % 3 == 1  # rows of zeros, with the large scale
+    a = rows(M, torch.where(empty, 0.0, 448.0))
+    bg, bu = rows(N, torch.full((N,), 448.0, device="cuda")), rows(N, torch.where(n % 2 == 0, 448.0, -448.0))
+    sa = torch.where(empty, 1.3 * 2.0 ** 70, 1.1 * 2.0 ** -100)
+    s1 = torch.where(n % 2 == 0, 1.7 * 2.0 ** -52, 1.9 * 2.0 ** 70)
+    s2 = torch.where(n % 3 == 0, 1.5 * 2.0 ** 70, 1.3 * 2.0 ** -52)
+    G, U_, out = (torch.empty(M, N, device="cuda") for _ in range(3))
+    total = 448.0 * 448.0 * K  # (a multiple of 2^12 below 2^36: exact in any order)
+
+    def near(got, sign, scale, what):
+        want = torch.where(empty, 0.0, total)[:, None].double() * sign.double() * sa.double()[:, None] * scale.double()
+        off = (got.double() - want).abs() > want.abs() * (2 * bounds.U) + 2.0 ** -149
+        assert not bool((off | got.isnan()).any()), (what, int(off.sum()), int(got.isnan().sum()))
+    one, up = torch.ones(N, device="cuda"), torch.where(n % 2 == 0, 1.0, -1.0)
+    sg.gemm_e4m3_gated(a, sa, bg, s1, bu, s2, activation="none", pre_gate=G, pre_up=U_, out=out, workspace=workspace)
+    near(G, one, s1, "pre_gate")
+    near(U_, up, s2, "pre_up")
+    want = G.double() * U_.double()
+    assert bool(((out.double() - want).abs() <= want.abs() * bounds.U + 2.0 ** -149).all())
+    sg.gemm_e4m3_gated(a, sa, bg, None, bu, s2, activation="none", pre_gate=G, pre_up=U_, out=out, workspace=workspace)
+    near(G, one, one, "pre_gate without a column scale")
+    near(U_, up, s2, "pre_up beside it")
