@@ -190,7 +190,8 @@ def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation=
 
     `pre_gate` and `pre_up` hold what sgemm_gated() stored there.  Where the
     weights are the two halves of one tensor (side by side, or with `transb` one
-    below the other), dB_gate and dB_up are the halves of one tensor too.
+    below the other; the gate's first or second), dB_gate and dB_up are the
+    halves of one tensor too, in the same order.
     `workspace` as for sgemm(): one given as a tensor is used by the products,
     one after the other.
     """
@@ -210,28 +211,29 @@ def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation=
     act, tb = _activation(activation), 1 if transb else 0
     torch = _torch()
     # one tensor of both weights: its products are single ones of twice the size
-    merged = ldg == ldu and B_up.data_ptr() - B_gate.data_ptr() == 4 * N * (ldg if transb else 1) and \
-        (transb or ldg >= 2 * N)
-    # dG and dU side by side; halves that products read one by one start 16-byte aligned
+    apart = B_up.data_ptr() - B_gate.data_ptr()
+    merged = ldg == ldu and abs(apart) == 4 * N * (ldg if transb else 1) and (transb or ldg >= 2 * N)
+    swapped = merged and apart < 0  # (the gate's half is the second)
+    # dG and dU side by side in the weights' order; halves that products read one by one start 16-byte aligned
     half = N if merged else (N + 3) & ~3
     ld = max((2 * half + 3) & ~3, 4)
-    dA = dB = dB_gate = dB_up = dbias_gate = dbias_up = dz = z = up = bias = None
+    dA = dB = dB_gate = dB_up = dbias_gate = dbias_up = dz = z = dg = du = bias = None
     if "A" in need or "B" in need:
         dz = torch.empty_strided((M, 2 * half), (ld, 1), dtype=torch.float32, device=device)
         z = dz.data_ptr()
-        up = z + 4 * half
+        dg, du = (z + 4 * half, z) if swapped else (z, z + 4 * half)
     if "bias" in need:
         dbias_gate, dbias_up = _empty((N,), device), _empty((N,), device)
         bias = dbias_gate.data_ptr(), dbias_up.data_ptr()
-    _gate_grad(M, N, act, grad, ldy, pre_gate, ldpg, pre_up, ldpu, z, ld, up, ld, *(bias or (None, None)), device)
+    _gate_grad(M, N, act, grad, ldy, pre_gate, ldpg, pre_up, ldpu, dg, ld, du, ld, *(bias or (None, None)), device)
     a, k = A.data_ptr(), max(K, 1)
     if "A" in need:
         dA = _empty((M, K), device)
         if merged:
-            _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, B_gate.data_ptr(), ldg, 0, dA.data_ptr(), k, 0, workspace,
-                      device)
+            both = (B_up if swapped else B_gate).data_ptr()
+            _products(1, 0, 1 - tb, M, K, 2 * N, z, ld, 0, both, ldg, 0, dA.data_ptr(), k, 0, workspace, device)
         else:
-            _pair(1 - tb, M, K, N, z, up, ld, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu, dA.data_ptr(), k, workspace,
+            _pair(1 - tb, M, K, N, dg, du, ld, B_gate.data_ptr(), ldg, B_up.data_ptr(), ldu, dA.data_ptr(), k, workspace,
                   device)
     if "B" in need:
         if transb:
@@ -243,7 +245,8 @@ def sgemm_gated_backward(grad, A, B_gate, B_up, *, pre_gate, pre_up, activation=
         else:
             dB = _empty((2, K, N), device)
             _products(2, 1, 0, K, N, M, a, lda, 0, z, ld, half, dB.data_ptr(), max(N, 1), K * N, workspace, device)
-        dB_gate, dB_up = (dB[:, :N], dB[:, N:]) if merged and not transb else (dB[0], dB[1])
+        halves = (dB[:, :N], dB[:, N:]) if merged and not transb else (dB[0], dB[1])
+        dB_gate, dB_up = halves[::-1] if swapped else halves
     return dA, dB_gate, dB_up, dbias_gate, dbias_up
 
 

@@ -7,6 +7,7 @@ import torch
 import fp32_gemm_sgemm_amd as sg
 import layers_bounds as bounds
 import layers_cases
+import layers_ref
 import ops_ref
 from gpu_cases import note
 
@@ -139,3 +140,36 @@ def test_scales_whose_product_leaves_float32(case):
     sg.gemm_e4m3_gated(a, sa, bg, None, bu, s2, activation="none", pre_gate=G, pre_up=U_, out=out, workspace=workspace)
     near(G, one, one, "pre_gate without a column scale")
     near(U_, up, s2, "pre_up beside it")
+
+
+# ---- the gated block's gradient -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("tb", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 3, 5), (33, 65, 40), (70, 130, 96), (129, 257, 65), (300, 64, 100)])
+def test_gradient_of_weights_with_the_gate_second(M, N, K, tb, pad):
+    """One tensor of both weights, the gate's the second half: the gradients are
+    halves of one tensor in the weights' order."""
+    note(f"gate second {M}x{N}x{K} tb={tb} pad={pad}")
+    A, dy, G, U_ = normal(M, K, seed=1), normal(M, N, seed=2), normal(M, N, seed=3), normal(M, N, seed=4)
+    hu, hg = (normal(*((N, K) if tb else (K, N)), seed=i) for i in (5, 6))
+    host = np.concatenate([hu, hg], 0 if tb else 1)
+    both = torch.zeros(host.shape[0], host.shape[1] + pad, device="cuda")[:, :host.shape[1]].copy_(dev(host))
+    Bu, Bg = (both[:N], both[N:]) if tb else (both[:, :N], both[:, N:])
+    got = sg.sgemm_gated_backward(dev(dy), dev(A), Bg, Bu, pre_gate=dev(G), pre_up=dev(U_), activation="silu", transb=tb)
+    w = [f64(v) for v in (dy, A, G, U_)]
+    wg, wu = (f64(hg.T), f64(hu.T)) if tb else (f64(hg), f64(hu))
+    dA, dBg, dBu, ta, tg, tu = layers_ref.gated_backward(w[0], w[1], wg, wu, w[2], w[3], "silu")
+    _, _, sums_g, sums_u, _, _, tsg, tsu = layers_ref.gated_grad(w[0], w[2], w[3], "silu")
+    if tb:
+        dBg, dBu, tg, tu = dBg.T, dBu.T, tg.T, tu.T
+    for what, g, want, t in zip(("dA", "dB_gate", "dB_up", "dbias_gate", "dbias_up"), got, (dA, dBg, dBu, sums_g, sums_u),
+                                (ta, tg, tu, tsg, tsu)):
+        ops_ref.within(f64(g), want, t, what)
+    step = got[1].data_ptr() - got[2].data_ptr()
+    assert got[1].stride() == got[2].stride() and step == 4 * N * (K if tb else 1)
+    for need in (("A",), ("B",), ("bias",)):
+        part = sg.sgemm_gated_backward(dev(dy), dev(A), Bg, Bu, pre_gate=dev(G), pre_up=dev(U_), activation="silu",
+                                       transb=tb, need=need)
+        for x, y, name in zip(part, got, ("A", "B", "B", "bias", "bias")):
+            assert (x is not None) == (name in need) and (x is None or torch.equal(x, y))
