@@ -4,6 +4,11 @@
 //   n = sqrt(sum over tensors and elements of x^2),
 //   c = min(1, max_norm / (n + eps)),  y = c x
 //
+// A c below float32's normal range (large values under a small limit) is kept as
+// 2^-126 times a normal number and applied in two steps: the first is exact but for
+// results below all of float32, so y has the roundings of c and of the
+// product like any other.
+//
 // Squares and their sums are float64, where a float32's square is exact and
 // cannot overflow, at no cost: the kernels are bound by memory (two conversions
 // and sums an element against 4 bytes read).
@@ -169,11 +174,25 @@ __device__ __forceinline__ double clip_squares(const ClipArgs &a, const ClipTens
     return sum;
 }
 
+// c = first * second.
+struct ClipFactor {
+    float first, second;
+};
+
+// c of the sum of all squares.  (A norm of NaN gives NaN.)
+__device__ __forceinline__ ClipFactor clip_factor(const ClipArgs &a, double total)
+{
+    const double c = a.max_norm / (sqrt(total) + a.eps);
+    if (c >= 1.0) return {1.0f, 1.0f};
+    return c < 0x1p-126 ? ClipFactor{0x1p-126f, (float)(c * 0x1p126)} : ClipFactor{1.0f, (float)c};
+}
+
 // y = c x over the same chunks, from the last one back.
 template <int NT>
-__device__ __forceinline__ void clip_write(const ClipArgs &a, const ClipTensor *table, int first, int step, float c)
+__device__ __forceinline__ void clip_write(const ClipArgs &a, const ClipTensor *table, int first, int step,
+                                           const ClipFactor &c)
 {
-    if (first >= a.chunks || (a.in_place && c == 1.0f)) return;
+    if (first >= a.chunks || (a.in_place && c.second == 1.0f && c.first == 1.0f)) return;
     constexpr int G = kClipChunk / (4 * NT);
     ClipWalk w(table, a.count, a.chunks);
     int64_t k = first + (int64_t)((a.chunks - 1 - first) / step) * step;
@@ -189,21 +208,16 @@ __device__ __forceinline__ void clip_write(const ClipArgs &a, const ClipTensor *
                     v[j] = __builtin_nontemporal_load(reinterpret_cast<const f32x4u *>(w.e.x + ix + j * 4 * NT));
 #pragma unroll
                 for (int j = 0; j < G; ++j)
-                    __builtin_nontemporal_store(v[j] * c, reinterpret_cast<f32x4u *>(w.e.y + iy + j * 4 * NT));
+                    __builtin_nontemporal_store(v[j] * c.first * c.second, reinterpret_cast<f32x4u *>(w.e.y + iy + j * 4 * NT));
             },
             [&](int64_t ix, int64_t iy, int left) {
                 float v[4];
                 load_cols<4>(w.e.x + ix, 0, left, v);
-                store_row<4>(w.e.y + iy, 0, left, v, c, 0.0f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] *= c.first;
+                store_row<4>(w.e.y + iy, 0, left, v, c.second, 0.0f);
             });
     }
-}
-
-// c of the sum of all squares.  (A norm of NaN gives NaN.)
-__device__ __forceinline__ float clip_factor(const ClipArgs &a, double total)
-{
-    const double q = a.max_norm / (sqrt(total) + a.eps);
-    return q >= 1.0 ? 1.0f : (float)q;
 }
 
 // HERE: the table is in the launch's arguments, else in memory.

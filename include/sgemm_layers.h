@@ -220,8 +220,9 @@ typedef struct sgemm_tensor {
  *   norm     n, one float, or NULL.
  *   workspace  16-byte aligned, at least sgemm_clip_f32_workspace's bytes.
  * Squares and sums are float64, and the factor is taken from the unrounded n
- * and rounded once.  A NaN, or an infinity, anywhere makes n so: the factor is
- * then NaN, or 0.  Where every y is its x and the factor is 1 nothing is
+ * and rounded once, to float32's precision wherever it lies (what is stored of n
+ * is infinite past float32's range, the factor is not 0 then).  A NaN, or an
+ * infinity, anywhere makes n so: the factor is then NaN, or 0.  Where every y is its x and the factor is 1 nothing is
  * written.  Up to 96 tensors take two launches, or one if they are small; more take
  * one for every 96 besides.
  */

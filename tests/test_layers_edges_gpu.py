@@ -173,3 +173,24 @@ def test_gradient_of_weights_with_the_gate_second(M, N, K, tb, pad):
                                        transb=tb, need=need)
         for x, y, name in zip(part, got, ("A", "B", "B", "bias", "bias")):
             assert (x is not None) == (name in need) and (x is None or torch.equal(x, y))
+
+
+# ---- norms over many tensors ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("size", [2.0 ** 40, 1e30, 1e37])
+@pytest.mark.parametrize("limit", [1e-5, 1e-10, 1e-25, 1e-37])
+def test_clipping_by_factors_below_float32(size, limit):
+    """The factor of large values and a small limit is below float32's normal
+    range, or all of it; what it leaves of the values is not."""
+    for shapes in ([(1000,)], [(3, 5), (70000,), (9, 4097), (2000, 17)], [(i % 7 + 1,) for i in range(300)]):
+        host = [normal(*s, seed=i) * np.float32(size) for i, s in enumerate(shapes)]
+        n = np.sqrt(sum((f64(x) ** 2).sum() for x in host))
+        f = float(np.float32(limit)) / n
+        xs, outs = [dev(x) for x in host], [torch.empty(s, device="cuda") for s in shapes]
+        got = sg.clip_grad_norm(xs, limit, eps=0.0, out=outs)
+        sg.clip_grad_norm(xs, limit, eps=0.0)
+        assert n > 3.4e38 or abs(float(got) - n) <= 2 * bounds.U * n
+        for x, o, h in zip(xs, outs, host):
+            # the factor's rounding and the product's
+            ops_ref.within(f64(o), f64(h) * f, np.abs(f64(h) * f) * (2.01 * bounds.U) + 2.0 ** -148)
+            assert torch.equal(x, o)
