@@ -99,6 +99,37 @@ def test_row_sums_are_float64(D):
     ops_ref.within(f64(dx), X, tx, "dx")
 
 
+@pytest.mark.parametrize("D", [300, 1500, 3000, 6000, 9000, 20001])
+def test_layernorm_onto_its_operands(D):
+    """With weight and bias, to the bit: S onto X and onto R, Y onto X and onto R,
+    both at once, and S in place beside codes."""
+    rows = 9
+    x, r = normal(rows, D, seed=1) + np.float32(2), normal(rows, D, seed=2)
+    w, b = dev(normal(D, seed=3)), dev(normal(D, seed=4))
+    bits = lambda t: t.contiguous().view(torch.uint8)  # noqa: E731
+    want, s = sg.layernorm(dev(x), w, b, residual=dev(r))
+    q, scale, _ = sg.layernorm_e4m3(dev(x), w, b, residual=dev(r))
+    alone, _ = sg.layernorm(dev(x), w, b)
+    t = dev(x)
+    y, same = sg.layernorm(t, w, b, out=t)
+    assert y is t and same is t and torch.equal(t, alone)
+    for onto in (0, 1):
+        t = [dev(x), dev(r)]
+        y, got = sg.layernorm(t[0], w, b, residual=t[1], sum_out=t[onto])
+        assert got is t[onto] and torch.equal(got, s) and torch.equal(y, want), onto
+        assert np.array_equal(t[1 - onto].cpu().numpy(), (r, x)[onto])
+        t = [dev(x), dev(r)]
+        kept = torch.empty(rows, D, device="cuda")
+        y, got = sg.layernorm(t[0], w, b, residual=t[1], sum_out=kept, out=t[onto])
+        assert y is t[onto] and torch.equal(y, want) and torch.equal(kept, s), onto
+        t = [dev(x), dev(r)]
+        y, got = sg.layernorm(t[0], w, b, residual=t[1], sum_out=t[onto], out=t[1 - onto])
+        assert torch.equal(t[onto], s) and torch.equal(t[1 - onto], want), onto
+        t = [dev(x), dev(r)]
+        q2, scale2, got = sg.layernorm_e4m3(t[0], w, b, residual=t[1], sum_out=t[onto])
+        assert torch.equal(got, s) and torch.equal(bits(q2), bits(q)) and torch.equal(scale2, scale), onto
+
+
 # ---- the gated block of 8-bit operands ----------------------------------------------------------------
 
 # one size for each 8-bit kernel, whole and with K split, aligned and not
