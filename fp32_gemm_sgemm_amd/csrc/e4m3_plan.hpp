@@ -61,7 +61,6 @@ struct E4m3Plan {
     int kernel;  // a tile, or the streaming kernel -1 - i, or kE4m3None
     int splits, k_chunk;
     long long workspace_bytes;
-    double ns;  // its cost by the model
 };
 
 // What a gated block's plan counts besides, from memory that no cache holds.  With
@@ -88,16 +87,16 @@ struct E4m3Cold {
 constexpr E4m3Cold kE4m3Cold[kE4m3TileCount] = {{64, 1, 0.0}, {128, 2, 950.0}, {128, 3, 900.0}, {128, 5, 880.0}};
 constexpr int kE4m3ColdRows = 512;
 constexpr double kE4m3ColdBytesPerNs = 6000.0;
-// The streaming kernels of a gated block (in the order of kE4m3Skinny, up to 16 rows aside):
+// The streaming kernels of a gated block past 16 rows (kE4m3Skinny's from the second on):
 // fill_ns, per 1024 codes of K the time of a workgroup, and the stream's rate, both by the rows.
-constexpr double kE4m3GatedFillNs[kE4m3SkinnyCount] = {0.0, 5500.0, 8500.0};
+constexpr double kE4m3GatedFillNs[kE4m3SkinnyCount - 1] = {5500.0, 8500.0};
 constexpr double kE4m3GatedWgNs = 700.0, kE4m3GatedRowNs = 22.0;
 constexpr double kE4m3GatedBytesPerNs = 5000.0, kE4m3GatedBytesPerNsRow = 33.0;
 
-// gated: N counts the columns of both weights.
+// gated: N counts the columns of both weights, and M is past 16 rows.
 inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long ws, bool gated = false)
 {
-    E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0, 0.0};
+    E4m3Plan best = {kE4m3None, 1, K > 0 ? K : 1, 0};
     double best_t = -1.0;
     for (int i = 0; i < kE4m3SkinnyCount; ++i) {
         const E4m3Skinny &s = kE4m3Skinny[i];
@@ -105,10 +104,10 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
         const double per_cu = (double)ceil_div_ll(ceil_div_ll(N, 16), cus);
         const double work = (double)K / 1024.0 * per_cu * (s.wg_ns + s.row_ns * M),
                      stream = (double)N * K / kE4m3StreamBytesPerNs;
-        best = {-1 - i, 1, K > 0 ? K : 1, 0, 0.0};
+        best = {-1 - i, 1, K > 0 ? K : 1, 0};
         best_t = s.fill_ns + (work > stream ? work : stream);
         if (gated)
-            best_t = kE4m3GatedFillNs[i] +
+            best_t = kE4m3GatedFillNs[i - 1] +
                      std::max((double)K / 1024.0 * (kE4m3GatedWgNs + kE4m3GatedRowNs * M),
                               (double)N * K / (kE4m3GatedBytesPerNs - kE4m3GatedBytesPerNsRow * M));
         break;
@@ -140,12 +139,11 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
             if (splits > 1)
                 t += kE4m3ReduceNs + 4.0 * (splits + 1) * (double)M * (double)N / kReduceBytesPerNs;
             if (best_t < 0.0 || t < best_t) {
-                best = {i, splits, splits > 1 ? (int)per : K, bytes, 0.0};
+                best = {i, splits, splits > 1 ? (int)per : K, bytes};
                 best_t = t;
             }
         }
     }
-    best.ns = best_t;
     return best;
 }
 
@@ -157,7 +155,7 @@ inline E4m3Plan e4m3_plan(int M, int N, int K, int cus, bool aligned, long long 
 // against 29.5).
 inline E4m3Plan e4m3_gated_plan(int M, int N, int K, int cus, bool aligned, long long ws)
 {
-    if (M <= kE4m3Skinny[0].rows) return {-1, 1, K, 0, 0.0};
+    if (M <= kE4m3Skinny[0].rows) return {-1, 1, K, 0};
     const int wide = N <= kMaxDim / 2 ? 2 * N : kMaxDim;
     E4m3Plan p = e4m3_plan(M, wide, K, cus, aligned, ws, true);
     // (the halves' rows are padded one by one)
