@@ -206,6 +206,47 @@ def test_gradient_of_weights_with_the_gate_second(M, N, K, tb, pad):
             assert (x is not None) == (name in need) and (x is None or torch.equal(x, y))
 
 
+def stored(host, tb):
+    """float64 K x N weights of stored ones."""
+    return f64(host.T if tb else host)
+
+
+@pytest.mark.parametrize("order", ["one tensor, gate second", "gate at the higher address", "the same weights"])
+@pytest.mark.parametrize("tb", [False, True])
+def test_weights_in_any_place(tb, order):
+    """Forward in every form and backward with the gate's weights behind the other
+    ones (a batch of the two has a negative stride), and with the two the same."""
+    for M, N, K in ((70, 130, 96), (5, 260, 1100), (40, 2000, 50)):
+        note(f"{order} {M}x{N}x{K} tb={tb}")
+        shape = (N, K) if tb else (K, N)
+        hu, hg = normal(*shape, seed=5) * np.float32(K ** -0.5), normal(*shape, seed=6) * np.float32(K ** -0.5)
+        if order == "the same weights":
+            hu = hg
+            Bg = Bu = dev(hg)
+        elif order == "gate at the higher address":
+            buf = torch.zeros(2 * N * K + 8, device="cuda")
+            Bu, Bg = buf[:N * K].view(shape), buf[N * K + 8:].view(shape)
+            Bu.copy_(dev(hu))
+            Bg.copy_(dev(hg))
+        else:
+            both = dev(np.concatenate([hu, hg], 0 if tb else 1))
+            Bu, Bg = (both[:N], both[N:]) if tb else (both[:, :N], both[:, N:])
+        A, dy, G, U_ = normal(M, K, seed=1), normal(M, N, seed=2), normal(M, N, seed=3), normal(M, N, seed=4)
+        wg, wu = stored(hg, tb), stored(hu, tb)
+        Y, _, _, ty, _, _ = layers_ref.gated(f64(A), wg, wu, K)
+        ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+        for form in (sg.GATED_AUTO, *range(8)):
+            ops_ref.within(f64(sg.sgemm_gated(dev(A), Bg, Bu, transb=tb, form=form, workspace=ws)), Y, ty, f"form {form}")
+        w = [f64(v) for v in (dy, A, G, U_)]
+        dA, dBg, dBu, ta, tg, tu = layers_ref.gated_backward(w[0], w[1], wg, wu, w[2], w[3], "silu")
+        if tb:
+            dBg, dBu, tg, tu = dBg.T, dBu.T, tg.T, tu.T
+        for space in (True, False, ws):
+            got = sg.sgemm_gated_backward(dev(dy), dev(A), Bg, Bu, pre_gate=dev(G), pre_up=dev(U_), transb=tb, workspace=space)
+            for what, g, want, t in zip(("dA", "dB_gate", "dB_up"), got, (dA, dBg, dBu), (ta, tg, tu)):
+                ops_ref.within(f64(g), want, t, what)
+
+
 # ---- norms over many tensors ------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("size", [2.0 ** 40, 1e30, 1e37])
@@ -225,3 +266,47 @@ def test_clipping_by_factors_below_float32(size, limit):
             # the factor's rounding and the product's
             ops_ref.within(f64(o), f64(h) * f, np.abs(f64(h) * f) * (2.01 * bounds.U) + 2.0 ** -148)
             assert torch.equal(x, o)
+
+
+def test_clipping_partly_in_place():
+    """Some tensors are scaled onto themselves and some elsewhere in one call."""
+    host = [normal(300, 70, seed=1), normal(5000, seed=2), normal(9, 11, seed=3)]
+    xs = [dev(x) for x in host]
+    outs = [xs[0], torch.empty(5000, device="cuda"), xs[2]]
+    n = np.sqrt(sum((f64(x) ** 2).sum() for x in host))
+    for limit, f in ((1e9, 1.0), (0.25, 0.25 / n)):
+        sg.clip_grad_norm(xs, limit, eps=0.0, out=outs)
+        for o, h in zip(outs, host):
+            ops_ref.within(f64(o), f64(h) * f, np.abs(f64(h) * f) * (2.01 * bounds.U))
+    assert np.array_equal(xs[1].cpu().numpy(), host[1])
+
+
+def test_long_lists_in_graphs():
+    """A list whose table goes to the workspace, captured: every replay scales what
+    the memory holds then, as an eager call does; two graphs of one pool."""
+    shapes = [(i % 13 + 1, i % 7 + 1) for i in range(230)] + [(70000,)]
+    xs, outs = [torch.empty(s, device="cuda") for s in shapes], [torch.empty(s, device="cuda") for s in shapes]
+
+    def fill(seed):
+        for i, x in enumerate(xs):
+            x.copy_(torch.from_numpy(normal(*x.shape, seed=1000 * seed + i)))
+    fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        sg.clip_grad_norm(xs, 0.5, out=outs)
+    torch.cuda.current_stream().wait_stream(side)
+    a, b = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(a):
+        na = sg.clip_grad_norm(xs, 0.5, out=outs)
+    with torch.cuda.graph(b, pool=a.pool()):
+        nb = sg.clip_grad_norm(xs[::2], 0.25, out=outs[::2])
+    for i in range(1, 4):
+        fill(i)
+        for graph, norm, part, limit in ((a, na, slice(None), 0.5), (b, nb, slice(None, None, 2), 0.25)):
+            want = [torch.empty_like(x) for x in xs[part]]
+            n = sg.clip_grad_norm(xs[part], limit, out=want)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(n, norm) and all(torch.equal(o, w) for o, w in zip(outs[part], want))
