@@ -548,7 +548,9 @@ const E4m3TileKernel kE4m3GatedTiles[sgemm::kE4m3TileCount] = {
 // Up to 16 rows where 16 columns a workgroup leave compute units idle: 8 columns of each
 // weight (1 and 16 rows in a graph, microseconds, 16 and 8 columns: two weights of 1024 x
 // 4096 8.2 and 6.5, 10.0 and 8.1; 2048 x 8192 13.9 and 12.2, 15.9 and 13.3; with as many
-// workgroups as compute units, 4096 x 4096, 11.8 and 10.7, 12.0 and 13.0).
+// workgroups as compute units, 4096 x 4096, 11.8 and 10.7, 12.0 and 13.0).  The rule
+// goes by the columns alone, so a single row of just as many columns as that leaves
+// those 10% for what 16 rows would lose.
 const E4m3SkinnyKernel kE4m3GatedNarrow = {
     128, reinterpret_cast<const void *>(&sgemm::gemm_e4m3_skinny_kernel<2, 1, true, true>)};
 const E4m3SkinnyKernel kE4m3GatedSkinny[sgemm::kE4m3SkinnyCount] = {

@@ -162,7 +162,10 @@ size_t layernorm_rows_bytes(int rows) { return ((size_t)rows * sizeof(sgemm::LnR
 // norm's gradient, but at least 512 where there are so many rows, and at most as
 // many as share the chip, since each writes 2 D sums (microseconds, without their
 // sum: 8192 x 4096 with 768 and 1024 workgroups 100 and 105, 8192 x 8192 with
-// 256 and 1024 143 and 155, 515 x 2052 with 256 and 515 9.8 and 7.6).
+// 256 and 1024 143 and 155, 515 x 2052 with 256 and 515 9.8 and 7.6).  With their sum
+// a row each past 512 workgroups costs more than the second row that some of 512
+// take: calls of 600 x 2051 16.3 and 15.8, 768 x 4096 19.3 and 17.2, 1000 x 2051
+// 19.3 and 16.4, 515 x 2051 the same.
 long long layernorm_grad_wgs(const RowForm &f, int rows)
 {
     const long long at_once = f.nt >= 256 ? 1 : 256 / f.nt;

@@ -16,7 +16,8 @@
 // x 8192 x 2048, 137 GFLOP, takes 931 us on 256x256 tiles (148 TFLOP/s, matrix cores
 // busy 92% of the cycles), 944 on 128x128 and 1016 on 64x64; two plain products into
 // memory and a second pass 961.  Those win where the outputs have few tiles and K is
-// split: 515 x 2051 x 1023 takes 57 us so, and 63 on 64x64 tiles with 4-byte loads.
+// split: 515 x 2051 x 1023 takes 57 us so, and 60 to 61 on 64x64 tiles with 4-byte
+// loads, which the plan takes there: its model has the two 5% apart the other way.
 #pragma once
 
 #include <type_traits>

@@ -157,8 +157,11 @@ int sgemm_f32_pair_workspace(int transb, int M, int N, int K,
  *   Y       rows x D; it may be X's, R's memory when S is not.
  *   eps     >= 0, finite.  A constant row with eps == 0 gives NaN (0 / 0).
  * D >= 1, rows >= 0, both <= INT_MAX - 1024; every ld >= D.  The mean and the
- * squares are summed in float64, so no square overflows.  A row that holds an
- * infinity or NaN is NaN throughout.
+ * squares are summed in float64, so no square overflows.  S - mean(S) and the
+ * inverse root are float32: a value further from the mean than float32 reaches
+ * (3.4e38, with values of both signs near it) is infinite here, and rows whose
+ * root passes 2^126 lose bits of the inverse.  A row that holds an infinity or
+ * NaN is NaN throughout.
  */
 int sgemm_layernorm_f32(int rows, int D, const float *X, int ldx, const float *R, int ldr,
                         const float *w, const float *b, float eps, float *S, int lds, float *Y, int ldy,
@@ -187,7 +190,8 @@ int sgemm_layernorm_e4m3(int rows, int D, const float *X, int ldx, const float *
  *   workspace  16-byte aligned, at least what
  *           sgemm_layernorm_f32_grad_workspace gives; NULL with 0 bytes where
  *           dw and db are NULL.  Too little is refused.
- * A row's sums are float64, the sums over rows float32.
+ * A row's sums are float64, the sums over rows float32; mean(g) and mean(g * h)
+ * are rounded to float32, which holds them for rows of any size.
  * Other arguments as sgemm_layernorm_f32.
  */
 int sgemm_layernorm_f32_grad(int rows, int D, const float *dY, int ldy, const float *S, int lds,
